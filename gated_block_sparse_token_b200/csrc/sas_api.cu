@@ -856,4 +856,268 @@ sas_status sas_decode_step_host(const sas_config* cfg, const void* q_host, void*
   return launch_result(cudaMemcpyAsync(out_host, out_dev, out_bytes, cudaMemcpyDeviceToHost, s));
 }
 
+// ---------------------------------------------------------------- norms with rotation
+namespace {
+
+// Host checks of one sas_rows argument; `out` rows must not repeat.
+sas_status check_rows(const sas_rows* r, int64_t elem, int batch, int heads, long long tokens, bool out) {
+  if (r->data == nullptr || !aligned(r->data, 16)) return SAS_ERR_INVALID_ARG;
+  if (r->seq_stride < 0 || r->token_stride < 0 || r->head_stride < 0 || r->tokens < tokens)
+    return SAS_ERR_INVALID_ARG;
+  if (r->seq_stride * elem % 16 != 0 || r->token_stride * elem % 16 != 0 || r->head_stride * elem % 16 != 0)
+    return SAS_ERR_INVALID_ARG;
+  if (out && ((batch > 1 && r->seq_stride < kDim) || (heads > 1 && r->head_stride < kDim) ||
+              (tokens > 1 && r->token_stride < kDim)))
+    return SAS_ERR_INVALID_ARG;
+  return SAS_OK;
+}
+
+sas::RowsView rows_view(const sas_rows* r) {
+  sas::RowsView v{};
+  if (r != nullptr) {
+    v.data = r->data;
+    v.seq = r->seq_stride;
+    v.token = r->token_stride;
+    v.head = r->head_stride;
+  }
+  return v;
+}
+
+// One side (queries or keys) of the norm entry points: all given or none.
+sas_status check_norm_side(const sas_rows* x, const float* gamma, const sas_rows* y, const sas_rows* d,
+                           const float* dgamma, bool back, int64_t elem, int batch, int heads, int tokens,
+                           bool* used) {
+  *used = x != nullptr;
+  if (!*used) {
+    if (y != nullptr || d != nullptr) return SAS_ERR_INVALID_ARG;
+    return SAS_OK;
+  }
+  if (y == nullptr || gamma == nullptr || !aligned(gamma, 4)) return SAS_ERR_INVALID_ARG;
+  sas_status st = check_rows(x, elem, batch, heads, tokens, false);
+  if (st == SAS_OK) st = check_rows(y, elem, batch, heads, tokens, true);
+  if (st != SAS_OK || !back) return st;
+  if (d == nullptr || dgamma == nullptr || !aligned(dgamma, 4)) return SAS_ERR_INVALID_ARG;
+  return check_rows(d, elem, batch, heads, tokens, false);
+}
+
+sas_status norm_rope_call(const sas_config* cfg, const sas_rows* dq_out, const sas_rows* dk_out, const sas_rows* q,
+                          const sas_rows* k, const float* gamma_q, const float* gamma_k, const int32_t* positions,
+                          int32_t batch, int32_t seq_len, float rope_base, const sas_rows* yq, const sas_rows* yk,
+                          float* dgamma_q, float* dgamma_k, bool back, void* ws, size_t ws_bytes,
+                          sas_stream_t stream) {
+  sas_status st = check_config(cfg);
+  if (st != SAS_OK) return st;
+  if (!finite_pos(rope_base) || batch < 0 || seq_len < 0) return SAS_ERR_INVALID_ARG;
+  if (back && (ws == nullptr || !aligned(ws, 16) || ws_bytes < sas_qk_norm_rope_workspace_bytes()))
+    return SAS_ERR_WORKSPACE;
+  if (batch == 0 || seq_len == 0) return SAS_OK;
+  if (!aligned(positions, 4)) return SAS_ERR_INVALID_ARG;
+  if (static_cast<long long>(batch) * seq_len > (1LL << 30)) return SAS_ERR_UNSUPPORTED;
+  const bool f32 = cfg->kv_dtype == SAS_DTYPE_F32;
+  const int64_t elem = f32 ? 4 : 2;
+  bool has_q = false, has_k = false;
+  if ((st = check_norm_side(q, gamma_q, yq, dq_out, dgamma_q, back, elem, batch, cfg->num_q_heads, seq_len,
+                            &has_q)) != SAS_OK)
+    return st;
+  if ((st = check_norm_side(k, gamma_k, yk, dk_out, dgamma_k, back, elem, batch, cfg->num_kv_heads, seq_len,
+                            &has_k)) != SAS_OK)
+    return st;
+  if (!has_q && !has_k) return SAS_OK;
+  if (cfg->num_q_heads + cfg->num_kv_heads > 65535) return SAS_ERR_UNSUPPORTED;
+  sas::NormRopeParams p{};
+  sas::fill_rope_table(p.rope, rope_base);
+  p.batch = batch;
+  p.tokens = seq_len;
+  p.hq = has_q ? cfg->num_q_heads : 0;
+  p.hkv = has_k ? cfg->num_kv_heads : 0;
+  p.eps = cfg->norm_eps;
+  p.positions = positions;
+  p.x_q = rows_view(q);
+  p.x_k = rows_view(k);
+  p.y_q = rows_view(yq);
+  p.y_k = rows_view(yk);
+  p.d_q = rows_view(dq_out);
+  p.d_k = rows_view(dk_out);
+  p.gamma_q = gamma_q;
+  p.gamma_k = gamma_k;
+  p.ws_part = back ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes) : nullptr;
+  return launch_result(sas::launch_norm_rope(f32, back, p, dgamma_q, dgamma_k, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+sas_status sas_qk_norm_rope(const sas_config* cfg, const sas_rows* q, const sas_rows* k, const float* gamma_q,
+                            const float* gamma_k, const int32_t* positions, int32_t batch, int32_t seq_len,
+                            float rope_base, const sas_rows* q_out, const sas_rows* k_out, sas_stream_t stream) {
+  return norm_rope_call(cfg, nullptr, nullptr, q, k, gamma_q, gamma_k, positions, batch, seq_len, rope_base, q_out,
+                        k_out, nullptr, nullptr, false, nullptr, 0, stream);
+}
+
+size_t sas_qk_norm_rope_workspace_bytes(void) { return kStatusBytes + sas::norm_rope_scratch_bytes(); }
+
+sas_status sas_qk_norm_rope_backward(const sas_config* cfg, const sas_rows* dq_out, const sas_rows* dk_out,
+                                     const sas_rows* q, const sas_rows* k, const float* gamma_q, const float* gamma_k,
+                                     const int32_t* positions, int32_t batch, int32_t seq_len, float rope_base,
+                                     const sas_rows* dq, const sas_rows* dk, float* dgamma_q, float* dgamma_k,
+                                     void* ws, size_t ws_bytes, sas_stream_t stream) {
+  return norm_rope_call(cfg, dq_out, dk_out, q, k, gamma_q, gamma_k, positions, batch, seq_len, rope_base, dq, dk,
+                        dgamma_q, dgamma_k, true, ws, ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------- 8-bit cache
+namespace {
+
+// Checks every 8-bit cache call makes.  The caller handles batch 0.
+sas_status check_kv8(const sas_config* cfg, const sas_kv8* kv, const void* ws, size_t ws_bytes) {
+  sas_status st = check_config(cfg);
+  if (st != SAS_OK) return st;
+  if (kv == nullptr || kv->batch < 0) return SAS_ERR_INVALID_ARG;
+  if (kv->code != SAS_KV8_E4M3 && kv->code != SAS_KV8_INT8) return SAS_ERR_INVALID_ARG;
+  if ((st = check_ws(cfg, const_cast<void*>(ws), ws_bytes)) != SAS_OK) return st;
+  if (kv->batch == 0) return SAS_OK;
+  if (kv->k == nullptr || kv->v == nullptr || kv->k_scale == nullptr || kv->v_scale == nullptr ||
+      kv->k_tail == nullptr || kv->v_tail == nullptr || kv->seq_lens == nullptr)
+    return SAS_ERR_INVALID_ARG;
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || !aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4) ||
+      !aligned(kv->k_tail, 16) || !aligned(kv->v_tail, 16) || !aligned(kv->seq_lens, 4))
+    return SAS_ERR_INVALID_ARG;
+  if (kv->block_table != nullptr) {
+    if (!aligned(kv->block_table, 4) || kv->num_pages < 1 || kv->max_blocks_per_seq < 1) return SAS_ERR_INVALID_ARG;
+  } else {
+    if (kv->capacity < 64 || kv->capacity % 64 != 0) return SAS_ERR_INVALID_ARG;
+  }
+  if (static_cast<long long>(kv->batch) * cfg->num_kv_heads > 65535) return SAS_ERR_UNSUPPORTED;
+  return SAS_OK;
+}
+
+sas::Kv8View make_view8(const sas_config* cfg, const sas_kv8* kv) {
+  sas::Kv8View v{};
+  v.k = static_cast<const uint8_t*>(kv->k);
+  v.v = static_cast<const uint8_t*>(kv->v);
+  v.k_scale = kv->k_scale;
+  v.v_scale = kv->v_scale;
+  v.k_tail = static_cast<const __nv_bfloat16*>(kv->k_tail);
+  v.v_tail = static_cast<const __nv_bfloat16*>(kv->v_tail);
+  v.block_table = kv->block_table;
+  v.seq_lens = kv->seq_lens;
+  v.hkv = cfg->num_kv_heads;
+  v.blocks = kv->block_table != nullptr ? kv->max_blocks_per_seq : kv->capacity / 64;
+  v.num_pages = kv->num_pages;
+  return v;
+}
+
+}  // namespace
+
+sas_status sas_kv8_append(const sas_config* cfg, const sas_kv8* kv, const sas_rows* k_new, const sas_rows* v_new,
+                          const int32_t* new_starts, const int32_t* new_lens, int32_t max_new, void* ws,
+                          size_t ws_bytes, sas_stream_t stream) {
+  sas_status st = check_kv8(cfg, kv, ws, ws_bytes);
+  if (st != SAS_OK) return st;
+  if (max_new < 0) return SAS_ERR_INVALID_ARG;
+  if (kv->batch == 0 || max_new == 0) return SAS_OK;
+  if (cfg->kv_dtype != SAS_DTYPE_BF16) return SAS_ERR_UNSUPPORTED;
+  if (k_new == nullptr || v_new == nullptr || !aligned(new_starts, 4) || !aligned(new_lens, 4))
+    return SAS_ERR_INVALID_ARG;
+  if ((st = check_rows(k_new, 2, kv->batch, cfg->num_kv_heads, 0, false)) != SAS_OK) return st;
+  if ((st = check_rows(v_new, 2, kv->batch, cfg->num_kv_heads, 0, false)) != SAS_OK) return st;
+  sas::Kv8AppendParams p{};
+  p.kv = make_view8(cfg, kv);
+  p.k_new = rows_view(k_new);
+  p.v_new = rows_view(v_new);
+  p.new_tokens = k_new->tokens < v_new->tokens ? k_new->tokens : v_new->tokens;
+  p.new_starts = new_starts;
+  p.new_lens = new_lens;
+  p.max_new = max_new;
+  p.status = static_cast<uint32_t*>(ws);
+  return launch_result(sas::launch_kv8_append(kv->code, p, kv->batch, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+sas_status sas_kv8_read(const sas_config* cfg, const sas_kv8* kv, const int32_t* begin, int32_t count,
+                        const sas_rows* k_out, const sas_rows* v_out, void* ws, size_t ws_bytes,
+                        sas_stream_t stream) {
+  sas_status st = check_kv8(cfg, kv, ws, ws_bytes);
+  if (st != SAS_OK) return st;
+  if (count < 0) return SAS_ERR_INVALID_ARG;
+  if (kv->batch == 0 || count == 0 || (k_out == nullptr && v_out == nullptr)) return SAS_OK;
+  if (!aligned(begin, 4)) return SAS_ERR_INVALID_ARG;
+  const bool f32 = cfg->out_dtype == SAS_DTYPE_F32;
+  for (const sas_rows* r : {k_out, v_out})
+    if (r != nullptr && (st = check_rows(r, f32 ? 4 : 2, kv->batch, cfg->num_kv_heads, count, true)) != SAS_OK)
+      return st;
+  sas::Kv8ReadParams p{};
+  p.kv = make_view8(cfg, kv);
+  p.k_out = rows_view(k_out);
+  p.v_out = rows_view(v_out);
+  p.begin = begin;
+  p.count = count;
+  p.status = static_cast<uint32_t*>(ws);
+  return launch_result(sas::launch_kv8_read(kv->code, f32, p, kv->batch, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+sas_status sas_pool_keys_kv8(const sas_config* cfg, const sas_kv8* kv, const int32_t* blk_begin, int32_t num_blocks,
+                             const void* w_k, const float* gamma_k, void* gate_keys, int32_t max_gate_blocks,
+                             float* pooled_raw, void* ws, size_t ws_bytes, sas_stream_t stream) {
+  sas_status st = check_kv8(cfg, kv, ws, ws_bytes);
+  if (st != SAS_OK) return st;
+  if (num_blocks < 0 || max_gate_blocks < 1 || max_gate_blocks > kMaxGateBlocks) return SAS_ERR_INVALID_ARG;
+  if (kv->batch == 0 || num_blocks == 0) return SAS_OK;
+  if (w_k == nullptr || gamma_k == nullptr || gate_keys == nullptr) return SAS_ERR_INVALID_ARG;
+  if (!aligned(w_k, 16) || !aligned(gamma_k, 4) || !aligned(gate_keys, 16) || !aligned(pooled_raw, 4) ||
+      !aligned(blk_begin, 4))
+    return SAS_ERR_INVALID_ARG;
+  if (prepare() != cudaSuccess) return SAS_ERR_CUDA;
+  sas::PoolParams p{};
+  p.hkv = cfg->num_kv_heads;
+  p.mg = max_gate_blocks;
+  p.num_blocks = num_blocks;
+  p.rope_base = cfg->rope_base;
+  p.eps = cfg->norm_eps;
+  sas::fill_rope_table(p.rope, cfg->rope_base);
+  p.kv.k = kv->k;
+  p.kv.block_table = kv->block_table;
+  p.kv.seq_lens = kv->seq_lens;
+  p.kv.hkv = cfg->num_kv_heads;
+  p.kv.capacity = kv->capacity;
+  p.kv.num_pages = kv->num_pages;
+  p.kv.max_blocks_per_seq = kv->max_blocks_per_seq;
+  p.k_scale = kv->k_scale;
+  p.blk_begin = blk_begin;
+  p.w_k = static_cast<const __nv_bfloat16*>(w_k);
+  p.gamma_k = gamma_k;
+  p.gate_keys = gate_keys;
+  p.gk16 = cfg->gate_keys_bf16;
+  p.pooled_raw = pooled_raw;
+  p.status = static_cast<uint32_t*>(ws);
+  CUtensorMap tmwk;
+  if (!encode_kv_map(&tmwk, w_k, static_cast<long long>(cfg->num_kv_heads) * sas::kPool)) return SAS_ERR_CUDA;
+  return launch_result(
+      sas::launch_pool_project_kv8(kv->code, p, tmwk, kv->batch, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+sas_status sas_sparse_decode_kv8(const sas_config* cfg, const void* q, const sas_kv8* kv, const int32_t* sel_idx,
+                                 const int32_t* sel_count, void* out, void* ws, size_t ws_bytes,
+                                 sas_stream_t stream) {
+  sas_status st = check_kv8(cfg, kv, ws, ws_bytes);
+  if (st != SAS_OK) return st;
+  if (kv->batch == 0) return SAS_OK;
+  if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 4)) return SAS_ERR_INVALID_ARG;
+  if ((sel_idx == nullptr) != (sel_count == nullptr) || !aligned(sel_idx, 4) || !aligned(sel_count, 4))
+    return SAS_ERR_INVALID_ARG;
+  if (cfg->kv_dtype != SAS_DTYPE_BF16) return SAS_ERR_UNSUPPORTED;
+  if (cfg->gate_mode != SAS_GATE_SELECT_ONLY) return SAS_ERR_UNSUPPORTED;
+  sas::Kv8AttendParams p{};
+  p.kv = make_view8(cfg, kv);
+  p.hq = cfg->num_q_heads;
+  p.G = cfg->num_q_heads / cfg->num_kv_heads;
+  p.max_sel = cfg->token_budget / 64;
+  p.scale_log2 = cfg->attn_scale * sas::kLog2e;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.sel_idx = sel_idx;
+  p.sel_count = sel_count;
+  p.out = out;
+  p.status = static_cast<uint32_t*>(ws);
+  return launch_result(sas::launch_kv8_attend(kv->code, cfg->out_dtype == SAS_DTYPE_F32, p, kv->batch,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

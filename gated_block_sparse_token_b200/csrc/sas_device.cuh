@@ -473,6 +473,55 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// ---------------------------------------------------------------- 8-bit codes
+enum Kv8Code : int { kCodeE4m3 = 0, kCodeInt8 = 1 };
+
+// Two e4m3 codes as f16x2;
+// exact.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  return r;
+}
+
+// Four codes of one word as two f16x2 (exact).  int8: the byte with its sign
+// bit flipped is code + 128; placed under the exponent byte 0x64 it reads as
+// the f16 number 1024 + code + 128.
+template <int CODE>
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (CODE == kCodeE4m3) {
+    lo = e4m3x2_f16x2(static_cast<uint16_t>(w & 0xffffu));
+    hi = e4m3x2_f16x2(static_cast<uint16_t>(w >> 16));
+  } else {
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    const uint32_t bias = 0x64806480u;  // 1152, twice
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(bias));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(bias));
+  }
+}
+
+__device__ __forceinline__ float f16_lo(uint32_t x) {
+  float r;
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %1; cvt.f32.f16 %0, a;}" : "=f"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float f16_hi(uint32_t x) {
+  float r;
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %1; cvt.f32.f16 %0, b;}" : "=f"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Monotone map float -> uint32 (larger float, larger key).  -0 maps like +0;
 // NaN maps below every number.
 __device__ __forceinline__ uint32_t order_key(float x) {

@@ -188,6 +188,7 @@ struct PoolParams {
   int gk16;
   float* pooled_raw;
   uint32_t* status;
+  const float* k_scale;  // 8-bit caches: one scale per 64-row tile of kv.k
 };
 
 struct PrefillParams {
@@ -360,6 +361,124 @@ cudaError_t launch_gate_backward(const GateBwdParams& p, const CUtensorMap& tmk,
                                  const CUtensorMap& tmwk, cudaStream_t stream);
 cudaError_t launch_prefill_gate_backward(const PrefillBwdParams& p, const CUtensorMap& tmq, const CUtensorMap& tmk,
                                          const CUtensorMap& tmv, cudaStream_t stream);
+
+// ---------------------------------------------------------------- norms with rotation
+// Rows of 128 elements of a [sequence][head][token] tensor with any strides
+// (in elements).
+struct RowsView {
+  const void* data;
+  long long seq, token, head;
+};
+
+constexpr int kNrThreads = 256;
+constexpr int kNrMaxCtas = 148 * 8;  // CTAs of the gradient pass (one partial row each)
+
+struct NormRopeParams {
+  RopeTable rope;
+  int batch, tokens, hq, hkv;  // hq or hkv 0: that side is left out
+  int chunk, q_chunks;         // heads of a CTA; chunks of query heads
+  float eps;
+  const int32_t* positions;    // [batch][tokens], or null: t
+  RowsView x_q, x_k, y_q, y_k; // input; output (forward: y, gradient: dx)
+  RowsView d_q, d_k;           // gradient: dy
+  const float* gamma_q;
+  const float* gamma_k;
+  float* ws_part;              // gradient: [chunks][grid.x][128]
+};
+
+struct NormRopeGrid {
+  int x, chunk, q_chunks, k_chunks;
+};
+
+// Heads of a CTA: as many as leave about two waves of full SMs (148 SMs x 8
+// CTAs of 256 threads), so that the angles are shared by many heads of a long
+// batch while a decode step's few rows spread over the SMs.  The gradient
+// keeps at most kNrMaxCtas CTAs, which then walk the tokens.
+inline NormRopeGrid norm_rope_grid(int batch, int tokens, int hq, int hkv, bool back) {
+  const long long slots = (static_cast<long long>(batch) * tokens + kNrThreads / 8 - 1) / (kNrThreads / 8);
+  const int most = std::max(std::max(hq, hkv), 1);
+  const long long want = slots * (hq + hkv) / (148 * 16);
+  NormRopeGrid g{};
+  g.chunk = static_cast<int>(std::min<long long>(std::max<long long>(want, 1), std::min(most, 8)));
+  for (;; ++g.chunk) {
+    g.q_chunks = (hq + g.chunk - 1) / g.chunk;
+    g.k_chunks = (hkv + g.chunk - 1) / g.chunk;
+    if (!back || g.q_chunks + g.k_chunks <= kNrMaxCtas || g.chunk >= most) break;
+  }
+  g.x = static_cast<int>(slots);
+  if (back) g.x = static_cast<int>(std::min<long long>(slots, std::max(kNrMaxCtas / (g.q_chunks + g.k_chunks), 1)));
+  return g;
+}
+
+// Bytes of the gradient's partial sums (every shape).
+inline size_t norm_rope_scratch_bytes() { return static_cast<size_t>(kNrMaxCtas) * kDim * 4; }
+
+cudaError_t launch_norm_rope(bool f32, bool back, NormRopeParams p, float* dgamma_q, float* dgamma_k,
+                             cudaStream_t stream);
+
+// ---------------------------------------------------------------- 8-bit cache
+constexpr int kTile8Bytes = kBlock * kDim;  // codes of one (block, KV head) of K or V
+
+// Addressing of the 8-bit cache: tile t holds the 64 x 128 codes of one block
+// and KV head at t * 8192, its scale is scale[t]; the tail holds the current
+// block of every sequence in bf16.
+struct Kv8View {
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const __nv_bfloat16* k_tail;  // [B][Hkv][64][128]
+  const __nv_bfloat16* v_tail;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int32_t hkv;
+  int32_t blocks;     // contiguous: capacity / 64; paged: max_blocks_per_seq
+  int32_t num_pages;
+
+  __device__ __forceinline__ long long tile(int s, int h, int b) const {
+    if (b < 0 || b >= blocks) return -1;
+    if (block_table == nullptr) return (static_cast<long long>(s) * hkv + h) * blocks + b;
+    const int page = block_table[static_cast<long long>(s) * blocks + b];
+    if (page < 0 || page >= num_pages) return -1;
+    return static_cast<long long>(page) * hkv + h;
+  }
+};
+
+struct Kv8AppendParams {
+  Kv8View kv;
+  RowsView k_new, v_new;
+  long long new_tokens;        // token rows that k_new / v_new hold
+  const int32_t* new_starts;   // [B] first token row of each sequence, or null: 0
+  const int32_t* new_lens;     // [B], or null: max_new
+  int max_new;
+  uint32_t* status;
+};
+
+struct Kv8ReadParams {
+  Kv8View kv;
+  RowsView k_out, v_out;       // data null: not wanted
+  const int32_t* begin;        // [B], or null: 0
+  int count;
+  uint32_t* status;
+};
+
+struct Kv8AttendParams {
+  Kv8View kv;
+  int hq, G, max_sel;
+  float scale_log2;            // attn_scale * log2(e)
+  const __nv_bfloat16* q;      // [B][Hq][128]
+  const int32_t* sel_idx;      // [B][Hkv][max_sel], or null: every block
+  const int32_t* sel_count;
+  void* out;                   // [B][Hq][128]
+  uint32_t* status;
+};
+
+cudaError_t launch_kv8_append(int code, const Kv8AppendParams& p, int batch, cudaStream_t stream);
+cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int batch, cudaStream_t stream);
+cudaError_t launch_kv8_attend(int code, bool f32_out, const Kv8AttendParams& p, int batch, cudaStream_t stream);
+// pooling over the 8-bit cache: p.kv.k holds the codes, p.k_scale the scales
+cudaError_t launch_pool_project_kv8(int code, const PoolParams& p, const CUtensorMap& tmwk, int batch,
+                                    cudaStream_t stream);
 
 // One-time per-process set-up of kernel attributes.
 cudaError_t prepare_kernels();

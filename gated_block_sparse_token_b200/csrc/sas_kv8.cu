@@ -1,0 +1,701 @@
+// The 8-bit KV cache: quantising write, read-back and block-sparse decode
+// attention.
+//
+// A complete 64-token block of one KV head is stored as 64 x 128 codes (e4m3,
+// or int8) of its keys and of its values, each under one fp32 scale:
+//   a = max(max |x|, 2^-100);  scale = a / qmax (448, or 127);
+//   code = round-to-nearest-even(x * qmax / a)
+// (a block that holds a NaN or an infinity: scale NaN, codes 0, so that it
+// reads back as NaN).  The block of a sequence's last token stays in bf16 in
+// the sequence's tail: codes are written once, when the block completes, from
+// the bf16 values, so the cache does not depend on how many tokens came per
+// call.
+#include <type_traits>
+
+#include "sas_internal.h"
+
+namespace sas {
+
+namespace {
+
+constexpr float kQmaxE4m3 = 448.f, kQmaxInt8 = 127.f;
+constexpr uint32_t kMinAmaxBits = 0x0d800000u;  // 2^-100
+constexpr uint32_t kBf16Inf = 0x7f80u;
+
+__device__ __forceinline__ uint16_t cvt_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ---------------------------------------------------------------- write
+// One CTA per (block job, KV head, sequence): threads 0-127 the keys, 128-255
+// the values, 8 rows x 8 dims per thread in registers between the maximum and
+// the rounding, so a block is read once and its codes written once.  Job 0 also
+// writes the tail, after its block has read the tail's old rows.
+__device__ __forceinline__ uint4 load_new_row(const RowsView& r, long long tok, int h, int s, int d0) {
+  const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(r.data) + static_cast<long long>(s) * r.seq +
+                           tok * r.token + static_cast<long long>(h) * r.head + d0;
+  return *reinterpret_cast<const uint4*>(p);
+}
+
+template <int CODE>
+__global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int s = blockIdx.z, h = blockIdx.y;
+  const int half = threadIdx.x >> 7, tid = threadIdx.x & 127, lane = tid & 31;
+  const int L = p.kv.seq_lens[s];
+  const int n = p.new_lens != nullptr ? p.new_lens[s] : p.max_new;
+  const long long start = p.new_starts != nullptr ? p.new_starts[s] : 0;
+  const int L0 = L - n;
+  bool err = n < 0 || n > p.max_new || L0 < 0 || start < 0 || start + n > p.new_tokens ||
+             static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
+  if (!err && n == 0) return;  // uniform over the CTA, like every branch on n and L
+  const int b_first = err ? 0 : L0 / kBlock, b_done = err ? 0 : L / kBlock;  // completed: [b_first, b_done)
+  // a page out of range anywhere in the write skips the whole (sequence, head)
+  for (int b = b_first + static_cast<int>(threadIdx.x); b < b_done && !err; b += 256)
+    if (p.kv.tile(s, h, b) < 0) err = true;
+  __shared__ uint32_t amax_s[2][4];
+  if (__syncthreads_or(err)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(p.status, kStatusBounds);
+    return;
+  }
+  const RowsView src = half == 0 ? p.k_new : p.v_new;
+  __nv_bfloat16* tail = const_cast<__nv_bfloat16*>(half == 0 ? p.kv.k_tail : p.kv.v_tail) +
+                        (static_cast<long long>(s) * p.kv.hkv + h) * (kBlock * kDim);
+  const int d0 = 8 * (tid & 15), r0 = tid >> 4;  // 16 lanes a row, rows r0, r0 + 8, ..
+  const int b = b_first + static_cast<int>(blockIdx.x);
+  if (b < b_done) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = r0 + 8 * i;
+      const int t = b * kBlock + row - L0;  // index among the new tokens
+      x[i] = t < 0 ? *reinterpret_cast<const uint4*>(tail + row * kDim + d0)
+                   : load_new_row(src, start + t, h, s, d0);
+    }
+    uint32_t m = 0;  // two bf16 magnitudes
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m = __vmaxu2(m, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu));
+      m = __vmaxu2(m, __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+    }
+    m = max(m & 0xffffu, m >> 16);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) amax_s[half][tid >> 5] = m;
+    __syncthreads();
+    m = max(max(amax_s[half][0], amax_s[half][1]), max(amax_s[half][2], amax_s[half][3]));
+    const bool finite = m < kBf16Inf;
+    const uint32_t abits = finite ? max(m << 16, kMinAmaxBits) : 0x3f800000u;
+    const float a = __uint_as_float(abits);
+    constexpr float qmax = CODE == kCodeE4m3 ? kQmaxE4m3 : kQmaxInt8;
+    // Quotient x qmax / a to within its last bit, and exact where it is
+    // representable (so also where it lies half-way between two codes): a and
+    // x are first scaled by 2^(1-e), e the exponent of a, which keeps every
+    // term in range; then one correction step with the exact remainder.  A
+    // quotient of bf16 values that is no half-way point is at least 2^-16 of
+    // its value away from one, so the code is that of the exact quotient.
+    const float pw = __uint_as_float(((255u - (abits >> 23)) << 23));
+    const float an = a * pw, inv = 1.f / an;
+    const float R = qmax / an * pw, T = qmax * pw;
+    const long long tile = p.kv.tile(s, h, b);
+    uint8_t* dst = const_cast<uint8_t*>(half == 0 ? p.kv.k : p.kv.v) + tile * kTile8Bytes;
+    auto quot = [&](float v) {
+      const float q = v * R;
+      return fmaf(fmaf(-q, an, v * T), inv, q);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t c[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float y0 = quot(bf16_lo(w[2 * k])), y1 = quot(bf16_hi(w[2 * k]));
+        const float y2 = quot(bf16_lo(w[2 * k + 1])), y3 = quot(bf16_hi(w[2 * k + 1]));
+        if constexpr (CODE == kCodeE4m3) {
+          c[k] = static_cast<uint32_t>(cvt_e4m3x2(y0, y1)) | (static_cast<uint32_t>(cvt_e4m3x2(y2, y3)) << 16);
+        } else {
+          const uint32_t i0 = __float2int_rn(y0) & 0xff, i1 = __float2int_rn(y1) & 0xff;
+          const uint32_t i2 = __float2int_rn(y2) & 0xff, i3 = __float2int_rn(y3) & 0xff;
+          c[k] = i0 | (i1 << 8) | (i2 << 16) | (i3 << 24);
+        }
+      }
+      *reinterpret_cast<uint2*>(dst + (r0 + 8 * i) * kDim + d0) = finite ? make_uint2(c[0], c[1]) : make_uint2(0u, 0u);
+    }
+    if (tid == 0)
+      const_cast<float*>(half == 0 ? p.kv.k_scale : p.kv.v_scale)[tile] =
+          finite ? __fdiv_rn(a, qmax) : __uint_as_float(0x7fc00000u);
+  }
+  if (blockIdx.x == 0) {
+    __syncthreads();  // the tail's old rows have been read
+    const int c = (L - 1) / kBlock;
+    for (int row = r0 + max(0, (L0 - c * kBlock) & ~7); row < L - c * kBlock; row += 8) {
+      const int t = c * kBlock + row - L0;
+      if (t >= 0) *reinterpret_cast<uint4*>(tail + row * kDim + d0) = load_new_row(src, start + t, h, s, d0);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- read-back
+// One CTA per (64 output tokens, KV head, sequence), threads 0-127 the keys,
+// 128-255 the values; 8 lanes a row, 16 codes a lane.
+template <int CODE, typename OutT>
+__global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int s = blockIdx.z, h = blockIdx.y;
+  const int half = threadIdx.x >> 7, tid = threadIdx.x & 127;
+  const int L = p.kv.seq_lens[s];
+  const int begin = p.begin != nullptr ? p.begin[s] : 0;
+  const RowsView o = half == 0 ? p.k_out : p.v_out;
+  bool err = L < 1 || begin < 0 || static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
+  if (o.data != nullptr && !err) {
+    const int c = (L - 1) / kBlock;
+    const int d0 = 16 * (tid & 7);
+    const __nv_bfloat16* tail = (half == 0 ? p.kv.k_tail : p.kv.v_tail) +
+                                (static_cast<long long>(s) * p.kv.hkv + h) * (kBlock * kDim);
+    const uint8_t* codes = half == 0 ? p.kv.k : p.kv.v;
+    const float* scales = half == 0 ? p.kv.k_scale : p.kv.v_scale;
+    OutT* out = static_cast<OutT*>(const_cast<void*>(o.data)) + static_cast<long long>(s) * o.seq +
+                static_cast<long long>(h) * o.head + d0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = static_cast<int>(blockIdx.x) * kBlock + (tid >> 3) + 16 * i;
+      const long long pos = static_cast<long long>(begin) + t;
+      if (t >= p.count || pos >= L) continue;
+      const int b = static_cast<int>(pos / kBlock), row = static_cast<int>(pos % kBlock);
+      float x[16];
+      if (b == c) {
+        const uint4* w = reinterpret_cast<const uint4*>(tail + row * kDim + d0);
+        const uint4 w0 = w[0], w1 = w[1];
+        const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x[2 * k] = bf16_lo(u[k]);
+          x[2 * k + 1] = bf16_hi(u[k]);
+        }
+      } else {
+        const long long tile = p.kv.tile(s, h, b);
+        if (tile < 0) {
+          err = true;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = 0.f;
+        } else {
+          const float sc = scales[tile];
+          const uint4 w = *reinterpret_cast<const uint4*>(codes + tile * kTile8Bytes + row * kDim + d0);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t lo, hi;
+            codes_f16<CODE>(u[k], lo, hi);
+            x[4 * k] = f16_lo(lo) * sc;
+            x[4 * k + 1] = f16_hi(lo) * sc;
+            x[4 * k + 2] = f16_lo(hi) * sc;
+            x[4 * k + 3] = f16_hi(hi) * sc;
+          }
+        }
+      }
+      OutT* dst = out + static_cast<long long>(t) * o.token;
+      if constexpr (std::is_same_v<OutT, float>) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          reinterpret_cast<float4*>(dst)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          reinterpret_cast<uint4*>(dst)[k] =
+              make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
+                         pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
+      }
+    }
+  }
+  if (err) raise_status(p.status, kStatusBounds);
+}
+
+// ---------------------------------------------------------------- attention
+// out_g = sum_j softmax_j(q_g . k_j * scale) v_j over the tokens of the listed
+// blocks (or of every block), one cluster of CTAs per (sequence, KV head).
+//
+// Bound by memory: 16 KiB of codes a block.  Each warp takes 16 keys of a
+// block straight from global memory into registers (no shared memory, no
+// barrier in the loop), the next block's loads in flight while one is used:
+//   S^T = K q^T  m16n8k16 f16: the 16 keys are the rows, the (up to 8) heads
+//                of the group the columns; codes are exact in f16, and the
+//                query is scaled by a power of two per head into f16's range
+//                (its bf16 values stay exact down to 2^-24 of the largest);
+//   softmax      per head over the columns, fp32, base 2; the running maximum
+//                moves only when it grows by more than 2^8 (any factor common
+//                to p and its sum cancels), so most blocks need one vote and
+//                no shuffles;
+//   O^T += V^T P^T, the P fragment transposed in place by movmatrix.  P is
+//                rounded to f16 (2^-12 relative, before a bf16 output); for an
+//                fp32 output a second product carries the remainder.  The sum
+//                runs over the unrounded p.
+// Both products take their k index from whatever order makes a lane's 16-byte
+// load its fragment: dims 16t .. 16t+15 and 64 + those for K, dims 16g .. of
+// four keys for V.  The block's two scales enter as fp32 factors of S and O.
+// The current block comes from the bf16 tail on bf16 products (P as a sum of
+// two bf16 terms), rows past the length masked.
+constexpr int kKaWarps = 4;
+constexpr int kKaHeadPair = 2 * kDim + 4;  // floats between head pairs of a partial (bank spread)
+constexpr int kKaPart = (kMaxGroup / 2) * kKaHeadPair;
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+__device__ __forceinline__ float ld_dsmem(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+struct KaFrag {
+  uint4 k[4];  // rows g, g + 8: dims 16t.., 64 + 16t..
+  uint4 v[4];  // keys 2t, 2t + 1, 2t + 8, 2t + 9: dims 16g..
+};
+
+struct KaState {
+  float m[2], l[2];   // heads 2t, 2t + 1 (m in the base-2 logit domain, uniform over g)
+  float acc[8][4];    // O^T: dims 16g + j (0, 1) and 16g + 8 + j (2, 3), heads 2t, 2t + 1
+};
+
+__device__ __forceinline__ float weight(float m, float top) { return m == -INFINITY ? 0.f : exp2_approx(m - top); }
+
+// Moves the running maximum to cover the 16 x 8 logits sc (this lane: keys
+// g, g + 8 x heads 2t, 2t + 1).
+__device__ __forceinline__ void raise_max(KaState& st, const float (&sc)[4]) {
+  const bool grow = fmaxf(sc[0], sc[2]) > st.m[0] + 8.f || fmaxf(sc[1], sc[3]) > st.m[1] + 8.f;
+  if (!__any_sync(0xffffffffu, grow)) return;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float x = fmaxf(sc[e], sc[e + 2]);
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+    const float top = fmaxf(st.m[e], x);
+    const float f = weight(st.m[e], top);
+    st.m[e] = top;
+    st.l[e] *= f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      st.acc[j][e] *= f;
+      st.acc[j][e + 2] *= f;
+    }
+  }
+}
+
+// One 16-key slice of a stored block.
+template <int CODE, bool SPLIT>
+__device__ __forceinline__ void attend_codes(KaState& st, const KaFrag& f, const uint32_t (&qf)[16],
+                                             const float (&qs)[2], float ks, float vs) {
+  float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t r0[4] = {f.k[2 * c].x, f.k[2 * c].y, f.k[2 * c].z, f.k[2 * c].w};
+    const uint32_t r1[4] = {f.k[2 * c + 1].x, f.k[2 * c + 1].y, f.k[2 * c + 1].z, f.k[2 * c + 1].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t a0, a1, a2, a3;
+      codes_f16<CODE>(r0[j], a0, a2);
+      codes_f16<CODE>(r1[j], a1, a3);
+      mma_f16(sc, a0, a1, a2, a3, qf[8 * c + 2 * j], qf[8 * c + 2 * j + 1]);
+    }
+  }
+  const float f0 = qs[0] * ks, f1 = qs[1] * ks;
+  sc[0] *= f0;
+  sc[1] *= f1;
+  sc[2] *= f0;
+  sc[3] *= f1;
+  raise_max(st, sc);
+  float p[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) p[e] = exp2_approx(sc[e] - st.m[e & 1]);
+  st.l[0] += p[0] + p[2];
+  st.l[1] += p[1] + p[3];
+  const uint32_t h0 = pack_f16x2(p[0], p[1]), h1 = pack_f16x2(p[2], p[3]);
+  const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
+  uint32_t e0 = 0, e1 = 0;
+  if constexpr (SPLIT) {
+    e0 = transpose8x8(pack_f16x2(p[0] - f16_lo(h0), p[1] - f16_hi(h0)));
+    e1 = transpose8x8(pack_f16x2(p[2] - f16_lo(h1), p[3] - f16_hi(h1)));
+  }
+  const uint32_t va[4] = {f.v[0].x, f.v[0].y, f.v[0].z, f.v[0].w};
+  const uint32_t vb[4] = {f.v[1].x, f.v[1].y, f.v[1].z, f.v[1].w};
+  const uint32_t vc[4] = {f.v[2].x, f.v[2].y, f.v[2].z, f.v[2].w};
+  const uint32_t vd[4] = {f.v[3].x, f.v[3].y, f.v[3].z, f.v[3].w};
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {  // dims 4w .. 4w + 3 and 8 + those of the lane's 16
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const uint32_t sel = hf == 0 ? 0x5140 : 0x7362;
+      uint32_t a0x, a0y, a1x, a1y, a2x, a2y, a3x, a3y;
+      codes_f16<CODE>(__byte_perm(va[w], vb[w], sel), a0x, a0y);
+      codes_f16<CODE>(__byte_perm(va[w + 2], vb[w + 2], sel), a1x, a1y);
+      codes_f16<CODE>(__byte_perm(vc[w], vd[w], sel), a2x, a2y);
+      codes_f16<CODE>(__byte_perm(vc[w + 2], vd[w + 2], sel), a3x, a3y);
+      const int j = 4 * w + 2 * hf;
+      float o[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_f16(o, a0x, a1x, a2x, a3x, b0, b1);
+      mma_f16(u, a0y, a1y, a2y, a3y, b0, b1);
+      if constexpr (SPLIT) {
+        mma_f16(o, a0x, a1x, a2x, a3x, e0, e1);
+        mma_f16(u, a0y, a1y, a2y, a3y, e0, e1);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        st.acc[j][e] = fmaf(o[e], vs, st.acc[j][e]);
+        st.acc[j + 1][e] = fmaf(u[e], vs, st.acc[j + 1][e]);
+      }
+    }
+  }
+}
+
+// One 16-key slice of the current block, from the bf16 tail: rows
+// row0 .. row0 + 15 of which those below `rows` count.
+__device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt, const __nv_bfloat16* vt,
+                                            const __nv_bfloat16* q, bool head_ok, int row0, int rows, float scale) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int d0 = 64 * c + 16 * t + 8 * i;
+      const uint4 r0 = *reinterpret_cast<const uint4*>(kt + (row0 + g) * kDim + d0);
+      const uint4 r1 = *reinterpret_cast<const uint4*>(kt + (row0 + g + 8) * kDim + d0);
+      const uint4 b = head_ok ? *reinterpret_cast<const uint4*>(q + d0) : make_uint4(0u, 0u, 0u, 0u);
+      mma_bf16_16816(sc, r0.x, r1.x, r0.y, r1.y, b.x, b.y);
+      mma_bf16_16816(sc, r0.z, r1.z, r0.w, r1.w, b.z, b.w);
+    }
+  }
+  const bool in0 = row0 + g < rows, in1 = row0 + g + 8 < rows;
+  sc[0] = in0 ? sc[0] * scale : -INFINITY;
+  sc[1] = in0 ? sc[1] * scale : -INFINITY;
+  sc[2] = in1 ? sc[2] * scale : -INFINITY;
+  sc[3] = in1 ? sc[3] * scale : -INFINITY;
+  raise_max(st, sc);
+  float p[4], lo[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    p[e] = (e < 2 ? in0 : in1) ? exp2_approx(sc[e] - st.m[e & 1]) : 0.f;
+    lo[e] = p[e] - __bfloat162float(__float2bfloat16_rn(p[e]));
+  }
+  st.l[0] += p[0] + p[2];
+  st.l[1] += p[1] + p[3];
+  const uint32_t b0 = transpose8x8(pack_bf16x2(p[0], p[1])), b1 = transpose8x8(pack_bf16x2(p[2], p[3]));
+  const uint32_t e0 = transpose8x8(pack_bf16x2(lo[0], lo[1])), e1 = transpose8x8(pack_bf16x2(lo[2], lo[3]));
+  uint32_t v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 2 * t + (i & 1) + 8 * (i >> 1);
+    const uint4* src = reinterpret_cast<const uint4*>(vt + row * kDim + 16 * g);
+    const uint4 x = src[0], y = src[1];
+    const bool in = row < rows;  // stale rows may hold anything, NaN included
+    v[i][0] = in ? x.x : 0u, v[i][1] = in ? x.y : 0u, v[i][2] = in ? x.z : 0u, v[i][3] = in ? x.w : 0u;
+    v[i][4] = in ? y.x : 0u, v[i][5] = in ? y.y : 0u, v[i][6] = in ? y.z : 0u, v[i][7] = in ? y.w : 0u;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t sel = (j & 1) ? 0x7632 : 0x5410;
+    const uint32_t a0 = __byte_perm(v[0][j / 2], v[1][j / 2], sel), a1 = __byte_perm(v[0][4 + j / 2], v[1][4 + j / 2], sel);
+    const uint32_t a2 = __byte_perm(v[2][j / 2], v[3][j / 2], sel), a3 = __byte_perm(v[2][4 + j / 2], v[3][4 + j / 2], sel);
+    mma_bf16_16816(st.acc[j], a0, a1, a2, a3, b0, b1);
+    mma_bf16_16816(st.acc[j], a0, a1, a2, a3, e0, e1);
+  }
+}
+
+}  // namespace
+
+template <int CODE, bool F32OUT>
+__global__ void __launch_bounds__(32 * kKaWarps) kv8_attend_kernel(const __grid_constant__ Kv8AttendParams p) {
+  __shared__ __align__(16) float part[kKaWarps][kKaPart];
+  __shared__ float ml[kKaWarps][2][kMaxGroup];
+  __shared__ float cta_ml[2][kMaxGroup];
+  __shared__ int cta_bad;
+  const int CS = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);
+  const int pair = static_cast<int>(blockIdx.y);
+  const int s = pair / p.kv.hkv, h = pair - s * p.kv.hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int G = p.G;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // ---- the list
+  const int L = p.kv.seq_lens[s];
+  bool bad = L < 1 || static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
+  const int c = bad ? 0 : (L - 1) / kBlock;
+  int m = c + 1;
+  const int32_t* sel = nullptr;
+  if (p.sel_idx != nullptr) {
+    m = p.sel_count[pair];
+    sel = p.sel_idx + static_cast<size_t>(pair) * p.max_sel;
+    if (m < 1 || m > p.max_sel) bad = true;
+    if (!bad && sel[m - 1] != c) bad = true;
+  }
+  // stored blocks of this CTA: entries rank, rank + CS, .. below m - 1; warp w
+  // takes keys 16w .. 16w + 15 of each
+  const int n = bad || rank >= m - 1 ? 0 : (m - 2 - rank) / CS + 1;
+
+  // ---- the query, as B fragments: head g, dims 16t .. and 64 + 16t ..
+  uint32_t qf[16];
+  float qs[2];
+  const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(s) * p.hq + static_cast<size_t>(h) * G + min(g, G - 1)) * kDim;
+  {
+    uint32_t raw[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(qrow + 64 * (i >> 1) + 16 * t + 8 * (i & 1));
+      raw[4 * i] = x.x, raw[4 * i + 1] = x.y, raw[4 * i + 2] = x.z, raw[4 * i + 3] = x.w;
+    }
+    uint32_t mag = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (g >= G) raw[i] = 0u;
+      mag = __vmaxu2(mag, raw[i] & 0x7fff7fffu);
+    }
+    mag = max(mag & 0xffffu, mag >> 16);
+    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+    // biased exponent e of the largest value (1 .. 254): q 2^(127-e) lies in [0, 2)
+    const uint32_t e = min(max(mag >> 7, 1u), 253u);
+    const float dn = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) qf[i] = pack_f16x2(bf16_lo(raw[i]) * dn, bf16_hi(raw[i]) * dn);
+    qs[0] = __shfl_sync(0xffffffffu, up, 8 * t) * p.scale_log2;
+    qs[1] = __shfl_sync(0xffffffffu, up, 8 * t + 4) * p.scale_log2;
+  }
+
+  KaState st;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    st.m[e] = -INFINITY;
+    st.l[e] = 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) st.acc[j][e] = 0.f;
+
+  // ---- stored blocks.  Lane l holds the tile and scales of the chunk's l-th
+  // entry; a tile out of range ends the warp's loop.
+  long long tile_c = 0, tile_n = 0;
+  float ks_c = 0.f, vs_c = 0.f, ks_n = 0.f, vs_n = 0.f;
+  auto fetch = [&](int i0, long long& tile, float& ks, float& vs) -> bool {  // entries i0 .. i0 + 31
+    const int i = i0 + lane;
+    bool ok = true;
+    tile = 0;
+    if (i < n) {
+      const int j = rank + CS * i;
+      const int b = sel != nullptr ? sel[j] : j;
+      if (sel != nullptr && sel[j + 1] <= b) ok = false;  // ascending, so every block is below c
+      tile = b < c ? p.kv.tile(s, h, b) : -1;
+      if (tile < 0) {
+        ok = false;
+        tile = 0;
+      }
+      if (ok) {
+        ks = p.kv.k_scale[tile];
+        vs = p.kv.v_scale[tile];
+      }
+    }
+    return __all_sync(0xffffffffu, ok);
+  };
+  auto load = [&](KaFrag& f, long long tile) {
+    const uint8_t* kp = p.kv.k + tile * kTile8Bytes + (16 * warp + g) * kDim + 16 * t;
+    f.k[0] = ld_stream(kp);
+    f.k[1] = ld_stream(kp + 8 * kDim);
+    f.k[2] = ld_stream(kp + 64);
+    f.k[3] = ld_stream(kp + 8 * kDim + 64);
+    const uint8_t* vp = p.kv.v + tile * kTile8Bytes + (16 * warp + 2 * t) * kDim + 16 * g;
+    f.v[0] = ld_stream(vp);
+    f.v[1] = ld_stream(vp + kDim);
+    f.v[2] = ld_stream(vp + 8 * kDim);
+    f.v[3] = ld_stream(vp + 9 * kDim);
+  };
+  int n_ok = n;  // entries whose tiles are known to be in range
+  if (n > 0) {
+    if (!fetch(0, tile_c, ks_c, vs_c)) {
+      bad = true;
+      n_ok = 0;
+    }
+  }
+  if (n_ok > 0) {
+    KaFrag f0, f1;
+    load(f0, __shfl_sync(0xffffffffu, tile_c, 0));
+    auto step = [&](int i, KaFrag& cur, KaFrag& nxt) {
+      if ((i & 31) == 0 && i + 32 < n_ok && !fetch(i + 32, tile_n, ks_n, vs_n)) {
+        bad = true;
+        n_ok = i + 32;
+      }
+      if (i + 1 < n_ok) load(nxt, __shfl_sync(0xffffffffu, (i & 31) == 31 ? tile_n : tile_c, (i + 1) & 31));
+      attend_codes<CODE, F32OUT>(st, cur, qf, qs, __shfl_sync(0xffffffffu, ks_c, i & 31),
+                                 __shfl_sync(0xffffffffu, vs_c, i & 31));
+      if ((i & 31) == 31) {
+        tile_c = tile_n;
+        ks_c = ks_n;
+        vs_c = vs_n;
+      }
+    };
+    for (int i = 0; i < n_ok; i += 2) {
+      step(i, f0, f1);
+      if (i + 1 < n_ok) step(i + 1, f1, f0);
+    }
+  }
+  // ---- the current block: the CTA whose turn it is
+  if (!bad && rank == (m - 1) % CS && 16 * warp < L - c * kBlock) {
+    const size_t off = static_cast<size_t>(pair) * (kBlock * kDim);
+    attend_tail(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * warp, L - c * kBlock, p.scale_log2);
+  }
+
+  // ---- merge: warps, then CTAs of the cluster
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 4);
+    st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 8);
+    st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 16);
+    if (g == 0) {
+      ml[warp][0][2 * t + e] = st.m[e];
+      ml[warp][1][2 * t + e] = st.l[e];
+    }
+    float* dst = &part[warp][t * kKaHeadPair + e * kDim + 16 * g];
+    float4* d4 = reinterpret_cast<float4*>(dst);
+    d4[0] = make_float4(st.acc[0][e], st.acc[1][e], st.acc[2][e], st.acc[3][e]);
+    d4[1] = make_float4(st.acc[4][e], st.acc[5][e], st.acc[6][e], st.acc[7][e]);
+    d4[2] = make_float4(st.acc[0][e + 2], st.acc[1][e + 2], st.acc[2][e + 2], st.acc[3][e + 2]);
+    d4[3] = make_float4(st.acc[4][e + 2], st.acc[5][e + 2], st.acc[6][e + 2], st.acc[7][e + 2]);
+  }
+  bad = __syncthreads_or(bad) != 0;
+  {
+    for (int hd = 0; hd < G; ++hd) {  // thread = dimension
+      float top = ml[0][0][hd];
+#pragma unroll
+      for (int w = 1; w < kKaWarps; ++w) top = fmaxf(top, ml[w][0][hd]);
+      float o = 0.f, l = 0.f;
+      const int at = (hd >> 1) * kKaHeadPair + (hd & 1) * kDim + tid;
+#pragma unroll
+      for (int w = 0; w < kKaWarps; ++w) {
+        const float f = weight(ml[w][0][hd], top);
+        o = fmaf(f, part[w][at], o);
+        l = fmaf(f, ml[w][1][hd], l);
+      }
+      part[0][at] = o;  // read and written by this thread alone
+      if (tid == 0) {
+        cta_ml[0][hd] = top;
+        cta_ml[1][hd] = l;
+      }
+    }
+    if (tid == 0) cta_bad = bad ? 1 : 0;
+  }
+  const auto store = [&](int hd, int d, float v) {
+    const size_t at = (static_cast<size_t>(s) * p.hq + static_cast<size_t>(h) * G + hd) * kDim + d;
+    if constexpr (F32OUT)
+      static_cast<float*>(p.out)[at] = v;
+    else
+      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  };
+  // every CTA's partial is complete and visible to the cluster
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int dpc = kDim / CS;
+  bool any_bad = false;
+  for (int r = 0; r < CS; ++r) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(dsmem_addr(&cta_bad, r)) : "memory");
+    any_bad = any_bad || v != 0;
+  }
+  for (int i = tid; i < G * dpc; i += 32 * kKaWarps) {
+    const int hd = i / dpc, d = rank * dpc + i % dpc;
+    const int at = (hd >> 1) * kKaHeadPair + (hd & 1) * kDim + d;
+    float top = -INFINITY;
+    for (int r = 0; r < CS; ++r) top = fmaxf(top, ld_dsmem(dsmem_addr(&cta_ml[0][hd], r)));
+    float o = 0.f, l = 0.f;
+    for (int r = 0; r < CS; ++r) {
+      const float f = weight(ld_dsmem(dsmem_addr(&cta_ml[0][hd], r)), top);
+      o = fmaf(f, ld_dsmem(dsmem_addr(&part[0][at], r)), o);
+      l = fmaf(f, ld_dsmem(dsmem_addr(&cta_ml[1][hd], r)), l);
+    }
+    store(hd, d, any_bad ? 0.f : o / l);
+  }
+  if (any_bad && rank == 0 && tid == 0) raise_status(p.status, kStatusBounds);
+  // no CTA leaves while another may still read its shared memory
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- launches
+namespace {
+
+template <typename P>
+cudaError_t launch(void (*k)(P), dim3 grid, int threads, int cluster, cudaStream_t stream, const P& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  a[1].val.clusterDim.y = 1;
+  a[1].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(int code, const Kv8AppendParams& p, int batch, cudaStream_t stream) {
+  // at most (63 + max_new) / 64 blocks are completed
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.max_new) + kBlock - 1) / kBlock),
+                  static_cast<unsigned>(p.kv.hkv), static_cast<unsigned>(batch));
+  return code == kCodeE4m3 ? launch(kv8_append_kernel<kCodeE4m3>, grid, 256, 0, stream, p)
+                           : launch(kv8_append_kernel<kCodeInt8>, grid, 256, 0, stream, p);
+}
+
+cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int batch, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.count) + kBlock - 1) / kBlock),
+                  static_cast<unsigned>(p.kv.hkv), static_cast<unsigned>(batch));
+  if (code == kCodeE4m3)
+    return f32_out ? launch(kv8_read_kernel<kCodeE4m3, float>, grid, 256, 0, stream, p)
+                   : launch(kv8_read_kernel<kCodeE4m3, __nv_bfloat16>, grid, 256, 0, stream, p);
+  return f32_out ? launch(kv8_read_kernel<kCodeInt8, float>, grid, 256, 0, stream, p)
+                 : launch(kv8_read_kernel<kCodeInt8, __nv_bfloat16>, grid, 256, 0, stream, p);
+}
+
+cudaError_t launch_kv8_attend(int code, bool f32_out, const Kv8AttendParams& p, int batch, cudaStream_t stream) {
+  const int cs = 8;
+  const dim3 grid(static_cast<unsigned>(cs), static_cast<unsigned>(batch * p.kv.hkv));
+  constexpr int T = 32 * kKaWarps;
+  if (code == kCodeE4m3)
+    return f32_out ? launch(kv8_attend_kernel<kCodeE4m3, true>, grid, T, cs, stream, p)
+                   : launch(kv8_attend_kernel<kCodeE4m3, false>, grid, T, cs, stream, p);
+  return f32_out ? launch(kv8_attend_kernel<kCodeInt8, true>, grid, T, cs, stream, p)
+                 : launch(kv8_attend_kernel<kCodeInt8, false>, grid, T, cs, stream, p);
+}
+
+}  // namespace sas

@@ -1,0 +1,237 @@
+// Per-head RMSNorm of queries and keys with the position rotation in the same
+// pass, and its gradient.
+//
+//   x^ = x / sqrt(mean_d x_d^2 + eps)           (one row = one token and head)
+//   z  = gamma * x^
+//   y_i = z_i cos - z_(i+64) sin,  y_(i+64) = z_(i+64) cos + z_i sin,
+//         angle = pos * base^(-2i/128), i = 0 .. 63
+// gradient, for dL/dy:
+//   dz = rotation transposed of dy;  dgamma += dz * x^ (all rows);
+//   u = gamma * dz;  dx = (u - x^ * mean_d(u x^)) / sqrt(mean x^2 + eps)
+//
+// Both are bound by memory: a row is read and written once (the gradient
+// reads x and dy).  Eight lanes hold a row: lane j dims 8j .. 8j+7 and their
+// rotate-half partners 64 + 8j .. 64 + 8j + 7, so the rotation needs no
+// exchange and the mean one 8-lane reduction (three shuffles).  An 8-lane group
+// keeps its token's 8 (cos, sin) pairs in registers over a chunk of heads:
+// the angles are reduced in double precision (exact for any int32 position)
+// and would otherwise cost more than the row.
+#include "sas_internal.h"
+
+namespace sas {
+
+namespace {
+
+constexpr int kNrRowsPerCta = kNrThreads / 8;  // token slots of a CTA
+
+// 8 consecutive elements as fp32 (16-byte aligned).
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  x[0] = bf16_lo(r.x), x[1] = bf16_hi(r.x), x[2] = bf16_lo(r.y), x[3] = bf16_hi(r.y);
+  x[4] = bf16_lo(r.z), x[5] = bf16_hi(r.z), x[6] = bf16_lo(r.w), x[7] = bf16_hi(r.w);
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+__device__ __forceinline__ float sum8lanes(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  return v;
+}
+
+}  // namespace
+
+// blockIdx.y: a chunk of p.chunk heads, the query heads' chunks first (a
+// chunk never mixes queries and keys); blockIdx.x: tokens, 32 at a time.
+template <typename T, bool kBack>
+__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, j = lane & 7;
+  const bool is_q = static_cast<int>(blockIdx.y) < p.q_chunks;
+  const int h0 = (is_q ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y) - p.q_chunks) * p.chunk;
+  const int h1 = min(h0 + p.chunk, is_q ? p.hq : p.hkv);
+  const RowsView xv = is_q ? p.x_q : p.x_k, yv = is_q ? p.y_q : p.y_k, dv = is_q ? p.d_q : p.d_k;
+  const float* gamma = is_q ? p.gamma_q : p.gamma_k;
+  float glo[8], ghi[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    glo[e] = gamma[8 * j + e];
+    ghi[e] = gamma[64 + 8 * j + e];
+  }
+  float alo[8], ahi[8];  // gradient: this lane's share of dgamma
+#pragma unroll
+  for (int e = 0; e < 8; ++e) alo[e] = ahi[e] = 0.f;
+
+  const int n_tok = p.batch * p.tokens;
+  for (int n0 = static_cast<int>(blockIdx.x) * kNrRowsPerCta; n0 < n_tok;
+       n0 += static_cast<int>(gridDim.x) * kNrRowsPerCta) {
+    const int n = n0 + (tid >> 3);
+    const int s = n / p.tokens, t = n - s * p.tokens;
+    const int pos = n < n_tok ? (p.positions != nullptr ? p.positions[n] : t) : -1;
+    const bool live = pos >= 0;  // uniform over the 8 lanes of a row
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rope_cos_sin(p.rope.theta_over_pi[8 * j + e], max(pos, 0), cs[e], sn[e]);
+    const long long off = static_cast<long long>(s) * xv.seq + static_cast<long long>(t) * xv.token + 8 * j;
+    const T* x = static_cast<const T*>(xv.data) + off;
+    T* y = static_cast<T*>(const_cast<void*>(yv.data)) + static_cast<long long>(s) * yv.seq +
+           static_cast<long long>(t) * yv.token + 8 * j;
+    const T* dy = static_cast<const T*>(dv.data) + static_cast<long long>(s) * dv.seq +
+                  static_cast<long long>(t) * dv.token + 8 * j;
+#pragma unroll 2
+    for (int h = h0; h < h1; ++h) {
+      float lo[8], hi[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lo[e] = hi[e] = 0.f;
+      if (live) {
+        load8(x + h * xv.head, lo);
+        load8(x + h * xv.head + 64, hi);
+      }
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], ss));
+      const float r = rsqrtf(sum8lanes(ss) * (1.f / kDim) + p.eps);
+      if constexpr (!kBack) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = lo[e] * r * glo[e], b = hi[e] * r * ghi[e];
+          lo[e] = a * cs[e] - b * sn[e];
+          hi[e] = b * cs[e] + a * sn[e];
+        }
+      } else {
+        float dlo[8], dhi[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dlo[e] = dhi[e] = 0.f;
+        if (live) {
+          load8(dy + h * dv.head, dlo);
+          load8(dy + h * dv.head + 64, dhi);
+        }
+        float dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float zl = dlo[e] * cs[e] + dhi[e] * sn[e];
+          const float zh = dhi[e] * cs[e] - dlo[e] * sn[e];
+          lo[e] *= r;
+          hi[e] *= r;
+          alo[e] = fmaf(zl, lo[e], alo[e]);
+          ahi[e] = fmaf(zh, hi[e], ahi[e]);
+          dlo[e] = zl * glo[e];
+          dhi[e] = zh * ghi[e];
+          dot = fmaf(dlo[e], lo[e], fmaf(dhi[e], hi[e], dot));
+        }
+        const float m = sum8lanes(dot) * (1.f / kDim);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          lo[e] = r * (dlo[e] - lo[e] * m);
+          hi[e] = r * (dhi[e] - hi[e] * m);
+        }
+      }
+      if (live) {
+        store8(y + h * yv.head, lo);
+        store8(y + h * yv.head + 64, hi);
+      }
+    }
+  }
+
+  if constexpr (kBack) {
+    // the CTA's sum per dimension: the four rows of a warp, then the warps,
+    // in a fixed order
+    __shared__ float part[kNrThreads / 32][kDim];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int o = 8; o < 32; o <<= 1) {
+        alo[e] += __shfl_xor_sync(0xffffffffu, alo[e], o);
+        ahi[e] += __shfl_xor_sync(0xffffffffu, ahi[e], o);
+      }
+    }
+    if (lane < 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        part[tid >> 5][8 * j + e] = alo[e];
+        part[tid >> 5][64 + 8 * j + e] = ahi[e];
+      }
+    }
+    __syncthreads();
+    if (tid < kDim) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kNrThreads / 32; ++w) v += part[w][tid];
+      p.ws_part[(static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kDim + tid] = v;
+    }
+  }
+}
+
+// dgamma += the CTAs' partial sums, in a fixed order.  CTA (i, which): 32
+// columns of the query (0) or key (1) gain; warp w sums rows w, w + 32, ..
+__global__ void __launch_bounds__(1024) norm_rope_gain_kernel(const float* part, int q_rows, int k_rows,
+                                                              float* dgamma_q, float* dgamma_k) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ float acc[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const bool is_q = blockIdx.y == 0;
+  float* out = is_q ? dgamma_q : dgamma_k;
+  const int rows = is_q ? q_rows : k_rows;
+  const float* src = part + (is_q ? 0 : static_cast<size_t>(q_rows) * kDim) + 32 * blockIdx.x + lane;
+  float v = 0.f;
+  for (int r = w; r < rows; r += 32) v += src[static_cast<size_t>(r) * kDim];
+  acc[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && rows > 0) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) t += acc[k][lane];
+    out[32 * blockIdx.x + lane] += t;
+  }
+}
+
+namespace {
+
+template <typename... Args>
+cudaError_t launch_pdl(void (*k)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(bool f32, bool back, NormRopeParams p, float* dgamma_q, float* dgamma_k,
+                             cudaStream_t stream) {
+  const NormRopeGrid g = norm_rope_grid(p.batch, p.tokens, p.hq, p.hkv, back);
+  p.chunk = g.chunk;
+  p.q_chunks = g.q_chunks;
+  const dim3 grid(static_cast<unsigned>(g.x), static_cast<unsigned>(g.q_chunks + g.k_chunks));
+  cudaError_t e;
+  if (!back) {
+    return f32 ? launch_pdl(norm_rope_kernel<float, false>, grid, kNrThreads, stream, p)
+               : launch_pdl(norm_rope_kernel<__nv_bfloat16, false>, grid, kNrThreads, stream, p);
+  }
+  e = f32 ? launch_pdl(norm_rope_kernel<float, true>, grid, kNrThreads, stream, p)
+          : launch_pdl(norm_rope_kernel<__nv_bfloat16, true>, grid, kNrThreads, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_rope_gain_kernel, dim3(kDim / 32, 2), 1024, stream,
+                    static_cast<const float*>(p.ws_part), g.q_chunks * g.x, g.k_chunks * g.x, dgamma_q, dgamma_k);
+}
+
+}  // namespace sas

@@ -238,12 +238,59 @@ void fill_rope_table(RopeTable& t, float base) {
 //      warps per lane quarter, each half the rotate-half pairs), applies
 //      RMSNorm, gamma_k and the gate RoPE at the block index, and stores the
 //      gate keys.
+// SRC: the cache's elements, bf16 or (an 8-bit cache) codes under one scale a
+// block.  Codes and their mean are pooled in units of the scale -- exact in
+// bf16, the mean as hi + lo -- and the epilogue multiplies u by the block's
+// scale, so the 8-bit form reads half the bytes and rounds nothing more.
 constexpr int kPpRows = 128;          // blocks per CTA (the MMA's M)
 constexpr int kPpThreads = 256;
 constexpr int kPpA = kPpRows * 512 * 2;           // A operand bytes (8 chunks of 16 KiB)
 constexpr int kPpB = kPool * kDim * 2;            // B operand bytes (2 N-halves of 48 KiB)
 constexpr int kPpSmem = kPpA + kPpB + 2 * kPpRows * 4 + 64 + 1024;
 
+enum PoolSource : int { kSrcE4m3 = kCodeE4m3, kSrcInt8 = kCodeInt8, kSrcBf16 };
+
+// Pooled codes of one 64-token tile: maximum, minimum (f16x2, exact) and sum
+// (fp32, exact: multiples of 2^-9 below 2^15) of dims 16 cvec .. 16 cvec + 15,
+// cvec = lane % 8, over all 64 rows, in every lane.
+template <int CODE>
+__device__ __forceinline__ void pool_codes(const uint8_t* tile, int lane, uint32_t (&mx)[8], uint32_t (&mn)[8],
+                                           float (&sm)[16]) {
+  const uint8_t* src = tile + (lane >> 3) * kDim + 16 * (lane & 7);
+  uint4 raw[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) raw[r] = *reinterpret_cast<const uint4*>(src + 4 * r * kDim);
+#pragma unroll
+  for (int v = 0; v < 16; ++v) sm[v] = 0.f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      uint32_t c[2];
+      codes_f16<CODE>(w[v], c[0], c[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        mx[2 * v + k] = r == 0 ? c[k] : max_f16x2(mx[2 * v + k], c[k]);
+        mn[2 * v + k] = r == 0 ? c[k] : min_f16x2(mn[2 * v + k], c[k]);
+        sm[4 * v + 2 * k] += f16_lo(c[k]);
+        sm[4 * v + 2 * k + 1] += f16_hi(c[k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      mx[v] = max_f16x2(mx[v], __shfl_xor_sync(0xffffffffu, mx[v], o));
+      mn[v] = min_f16x2(mn[v], __shfl_xor_sync(0xffffffffu, mn[v], o));
+    }
+#pragma unroll
+    for (int v = 0; v < 16; ++v) sm[v] += __shfl_xor_sync(0xffffffffu, sm[v], o);
+  }
+}
+
+template <int SRC>
 __global__ void __launch_bounds__(kPpThreads, 1) pool_project_kernel(const __grid_constant__ PoolParams p,
                                                                      const __grid_constant__ CUtensorMap tmwk) {
   const int s = blockIdx.z;
@@ -290,7 +337,59 @@ __global__ void __launch_bounds__(kPpThreads, 1) pool_project_kernel(const __gri
   }
 
   // ---- pooling into the A operand
-  {
+  if constexpr (SRC != kSrcBf16) {
+    bool err = false;
+    for (int i = warp; i < kPpRows; i += kPpThreads / 32) {  // warp-uniform
+      const long long row = row_of(i);
+      if (row == -2) err = true;
+      uint32_t mx[8], mn[8];
+      float sm[16];
+      if (row >= 0) {
+        pool_codes<SRC>(static_cast<const uint8_t*>(p.kv.k) + row * kDim, lane, mx, mn, sm);
+      } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) mx[v] = mn[v] = 0u;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) sm[v] = 0.f;
+      }
+      if (lane < 8) {
+        const int cvec = lane;  // dims 16 cvec ..: chunk 2 sec + cvec / 4, 16-byte units 2 (cvec % 4) and the next
+        uint32_t pk[4][8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const float m0 = sm[2 * v] * (1.f / kBlock), m1 = sm[2 * v + 1] * (1.f / kBlock);
+          const float g0 = __bfloat162float(__float2bfloat16_rn(m0)), g1 = __bfloat162float(__float2bfloat16_rn(m1));
+          pk[0][v] = pack_bf16x2(f16_lo(mx[v]), f16_hi(mx[v]));
+          pk[1][v] = pack_bf16x2(f16_lo(mn[v]), f16_hi(mn[v]));
+          pk[2][v] = pack_bf16x2(g0, g1);
+          pk[3][v] = pack_bf16x2(m0 - g0, m1 - g1);
+        }
+#pragma unroll
+        for (int sec = 0; sec < 4; ++sec) {
+          uint8_t* dst = sA + (2 * sec + (cvec >> 2)) * (kPpRows * 128) + i * 128;
+          const int j = 2 * (cvec & 3);
+          *reinterpret_cast<uint4*>(dst + ((j ^ (i & 7)) << 4)) =
+              make_uint4(pk[sec][0], pk[sec][1], pk[sec][2], pk[sec][3]);
+          *reinterpret_cast<uint4*>(dst + (((j + 1) ^ (i & 7)) << 4)) =
+              make_uint4(pk[sec][4], pk[sec][5], pk[sec][6], pk[sec][7]);
+        }
+        if (p.pooled_raw != nullptr && row >= 0) {
+          const float sc = p.k_scale[row / kBlock];
+          float* pr = p.pooled_raw + ((static_cast<size_t>(s) * p.hkv + h) * p.mg + (b0 + i)) * kPool + cvec * 16;
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {  // 4-byte aligned: scalar stores
+            pr[2 * v] = f16_lo(mx[v]) * sc;
+            pr[2 * v + 1] = f16_hi(mx[v]) * sc;
+            pr[kDim + 2 * v] = f16_lo(mn[v]) * sc;
+            pr[kDim + 2 * v + 1] = f16_hi(mn[v]) * sc;
+            pr[2 * kDim + 2 * v] = sm[2 * v] * (1.f / kBlock) * sc;
+            pr[2 * kDim + 2 * v + 1] = sm[2 * v + 1] * (1.f / kBlock) * sc;
+          }
+        }
+      }
+    }
+    if (err && lane == 0) raise_status(p.status, kStatusBounds);
+  } else {
     constexpr int TPR = 16;             // lanes per K row (16-byte loads)
     const int cvec = lane % TPR, par = lane / TPR;
     const __nv_bfloat16* kbase = static_cast<const __nv_bfloat16*>(p.kv.k);
@@ -406,12 +505,20 @@ __global__ void __launch_bounds__(kPpThreads, 1) pool_project_kernel(const __gri
     tmem_ld32(tl + 32 * hf, lo);       // columns 32 hf .. 32 hf + 31
     tmem_ld32(tl + 64 + 32 * hf, hi);  // their rotate-half partners
     tmem_wait_ld();
+    const long long row = row_of(i);
+    if constexpr (SRC != kSrcBf16) {
+      const float sc = row >= 0 ? p.k_scale[row / kBlock] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        lo[k] *= sc;
+        hi[k] *= sc;
+      }
+    }
     float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) ss = fmaf(lo[k], lo[k], fmaf(hi[k], hi[k], ss));
     ssq[hf * kPpRows + i] = ss;
     __syncthreads();
-    const long long row = row_of(i);
     if (row >= 0 && okm) {
       const int b = b0 + i;
       const float inv = 1.f / sqrtf((ssq[i] + ssq[kPpRows + i]) / kDim + p.eps);
@@ -456,12 +563,27 @@ __global__ void __launch_bounds__(kPpThreads, 1) pool_project_kernel(const __gri
 cudaError_t launch_pool_project(const PoolParams& p, const CUtensorMap& tmwk, int batch, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((p.num_blocks + kPpRows - 1) / kPpRows), static_cast<unsigned>(p.hkv),
                   static_cast<unsigned>(batch));
-  pool_project_kernel<<<grid, kPpThreads, kPpSmem, stream>>>(p, tmwk);
+  pool_project_kernel<kSrcBf16><<<grid, kPpThreads, kPpSmem, stream>>>(p, tmwk);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pool_project_kv8(int code, const PoolParams& p, const CUtensorMap& tmwk, int batch,
+                                    cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((p.num_blocks + kPpRows - 1) / kPpRows), static_cast<unsigned>(p.hkv),
+                  static_cast<unsigned>(batch));
+  if (code == kCodeE4m3)
+    pool_project_kernel<kSrcE4m3><<<grid, kPpThreads, kPpSmem, stream>>>(p, tmwk);
+  else
+    pool_project_kernel<kSrcInt8><<<grid, kPpThreads, kPpSmem, stream>>>(p, tmwk);
   return cudaGetLastError();
 }
 
 cudaError_t prepare_pool_project_kernel() {
-  return cudaFuncSetAttribute(pool_project_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
+  cudaError_t e = cudaFuncSetAttribute(pool_project_kernel<kSrcBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(pool_project_kernel<kSrcE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(pool_project_kernel<kSrcInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
 }
 
 }  // namespace sas

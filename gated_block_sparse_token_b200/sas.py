@@ -28,6 +28,10 @@ SAS_ERR_CUDA = 4
 SAS_ERR_DEVICE_BOUNDS = 5
 SAS_ERR_TIMEOUT = 6
 
+KV8_E4M3 = 0               # 8-bit cache codes
+KV8_INT8 = 1
+_CODES = {torch.float8_e4m3fn: KV8_E4M3, torch.int8: KV8_INT8}
+
 GATE_SELECT_ONLY = 0       # selected blocks weighted 1
 GATE_LOGSIGMOID_BIAS = 1   # + log(sigmoid(gate score)) on a selected historical block's logits
 
@@ -62,6 +66,19 @@ class _Kv(ctypes.Structure):
                 ("token_budgets", ctypes.c_void_p)]
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("tokens", ctypes.c_int64)]
+
+
+class _Kv8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_tail", ctypes.c_void_p), ("v_tail", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("capacity", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+                ("code", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -75,6 +92,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         cfgp, kvp = ctypes.POINTER(_Config), ctypes.POINTER(_Kv)
+        kv8p, rwp = ctypes.POINTER(_Kv8), ctypes.POINTER(_Rows)
         sigs = {
             "sas_abi_version": (i32, []),
             "sas_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -91,6 +109,14 @@ def lib() -> ctypes.CDLL:
                                                     sz, vp]),
             "sas_gate_backward": (ctypes.c_int, [cfgp, vp, kvp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
             "sas_prefill_block_sparse": (ctypes.c_int, [cfgp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]),
+            "sas_qk_norm_rope": (ctypes.c_int, [cfgp, rwp, rwp, vp, vp, vp, i32, i32, ctypes.c_float, rwp, rwp, vp]),
+            "sas_qk_norm_rope_workspace_bytes": (sz, []),
+            "sas_qk_norm_rope_backward": (ctypes.c_int, [cfgp, rwp, rwp, rwp, rwp, vp, vp, vp, i32, i32, ctypes.c_float,
+                                                         rwp, rwp, vp, vp, vp, sz, vp]),
+            "sas_kv8_append": (ctypes.c_int, [cfgp, kv8p, rwp, rwp, vp, vp, i32, vp, sz, vp]),
+            "sas_kv8_read": (ctypes.c_int, [cfgp, kv8p, vp, i32, rwp, rwp, vp, sz, vp]),
+            "sas_pool_keys_kv8": (ctypes.c_int, [cfgp, kv8p, vp, i32, vp, vp, vp, i32, vp, vp, sz, vp]),
+            "sas_sparse_decode_kv8": (ctypes.c_int, [cfgp, vp, kv8p, vp, vp, vp, vp, sz, vp]),
             "sas_prefill_gate_backward": (ctypes.c_int, [cfgp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp,
                                                          vp, vp, vp, vp, vp, sz, vp]),
         }
@@ -183,6 +209,94 @@ class KvCache:
         return _Kv(_ptr(self.k), _ptr(self.v), _ptr(self.block_table), _ptr(self.seq_lens),
                    self.batch, 0, int(self.k.shape[0]), int(self.block_table.shape[1]),
                    _ptr(self.token_budgets))
+
+
+@dataclass
+class KvCache8:
+    """Mirror of sas_kv8 holding the tensors alive.  The codes' dtype
+    (torch.float8_e4m3fn or torch.int8) selects the code.  block_table None:
+    codes [B][Hkv][capacity][128], scales [B][Hkv][capacity/64]; else paged
+    codes [num_pages][Hkv][64][128], scales [num_pages][Hkv].  Tails are bf16
+    [B][Hkv][64][128] and hold each sequence's current block."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    k_tail: torch.Tensor
+    v_tail: torch.Tensor
+    seq_lens: torch.Tensor
+    block_table: Optional[torch.Tensor] = None
+
+    @property
+    def batch(self) -> int:
+        return int(self.seq_lens.shape[0])
+
+    def c(self, cfg: Config) -> _Kv8:
+        """The C description, after checking every shape, dtype and layout the
+        library takes from the configuration."""
+        hkv, B = cfg.num_kv_heads, self.seq_lens.shape[0]
+        k, v, bt = self.k, self.v, self.block_table
+        code = _CODES.get(k.dtype)
+        if code is None or v.dtype != k.dtype:
+            raise ValueError(f"codes are {k.dtype} / {v.dtype}: both torch.float8_e4m3fn or both torch.int8 are wanted")
+        ks = k.shape
+        if len(ks) != 4 or ks != v.shape or ks[1] != hkv or ks[3] != 128:
+            raise ValueError(f"codes are {tuple(ks)} / {tuple(v.shape)} for {hkv} KV heads")
+        if bt is None:
+            if ks[0] != B or ks[2] % 64:
+                raise ValueError(f"contiguous codes are {tuple(ks)} for batch {B}")
+            want, cap, pages, width = (B, hkv, ks[2] // 64), ks[2], 0, 0
+        else:
+            if ks[2] != 64 or bt.dim() != 2 or bt.shape[0] != B:
+                raise ValueError(f"paged codes are {tuple(ks)} with a block table {tuple(bt.shape)} for batch {B}")
+            _i32("block_table", bt)
+            want, cap, pages, width = (ks[0], hkv), 0, ks[0], bt.shape[1]
+        if not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("codes must be contiguous")
+        _plain("k_scale", self.k_scale, want, torch.float32)
+        _plain("v_scale", self.v_scale, want, torch.float32)
+        _plain("k_tail", self.k_tail, (B, hkv, 64, 128), torch.bfloat16)
+        _plain("v_tail", self.v_tail, (B, hkv, 64, 128), torch.bfloat16)
+        _i32("seq_lens", self.seq_lens)
+        return _Kv8(k.data_ptr(), v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                    self.k_tail.data_ptr(), self.v_tail.data_ptr(), _ptr(bt), self.seq_lens.data_ptr(), B, cap, pages,
+                    width, code)
+
+    def tensors(self):
+        return (self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail, self.seq_lens, self.block_table)
+
+
+def _plain(name: str, t, shape, dtype) -> None:
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}{'' if t.is_contiguous() else ' (strided)'}: "
+                         f"contiguous {tuple(shape)} {dtype} is wanted")
+
+
+def _i32(name: str, t, n: Optional[int] = None) -> None:
+    if t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}: contiguous int32"
+                         + ("" if n is None else f" with {n} values") + " is wanted")
+
+
+def _rows(name: str, t, heads: int, dtype, batch: Optional[int] = None, tokens: Optional[int] = None) -> _Rows:
+    """sas_rows of a [B][H][T][128] tensor with any strides (last one 1)."""
+    sh = t.shape
+    if len(sh) != 4 or sh[1] != heads or sh[3] != 128 or t.dtype != dtype:
+        raise ValueError(f"{name} is {tuple(sh)} {t.dtype}: [B][{heads}][T][128] {dtype} is wanted")
+    if (batch is not None and sh[0] != batch) or (tokens is not None and sh[2] != tokens):
+        raise ValueError(f"{name} is {tuple(sh)}: batch {batch}, {tokens} tokens are wanted")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name}: the 128 elements of a row must be contiguous")
+    return _Rows(t.data_ptr(), st[0], st[2], st[1], sh[2])
+
+
+def _one_device(*tensors) -> None:
+    """Every tensor on the current CUDA device, where the library launches."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
 def abi_version() -> int:
@@ -341,6 +455,155 @@ def prefill_gate_backward(cfg: Config, q, k, v, w_q, gamma_q, w_k, gamma_k, gate
                                            int(gate_keys.shape[2]), _ptr(sel_idx), _ptr(sel_count), _ptr(d_out),
                                            _ptr(dw_q), _ptr(dw_k), _ptr(dgamma_q), _ptr(dgamma_k), _ptr(ws),
                                            ws.numel(), _stream(stream)), "sas_prefill_gate_backward")
+
+
+def qk_norm_rope(cfg: Config, q, k, gamma_q, gamma_k, q_out, k_out, rope_base: float, positions=None,
+                 stream=None) -> None:
+    """sas_qk_norm_rope: per-head RMSNorm and position rotation of q
+    [B][Hq][T][128] and k [B][Hkv][T][128] (cfg.kv_dtype, any strides with
+    contiguous rows) into q_out / k_out (may be q / k); q or k may be None.
+    positions: int32 [B][T] (negative: the row is skipped) or None (0 .. T-1)."""
+    dt = kv_dtype(cfg)
+    B, T = _batch_tokens(q, k)
+    args = [_norm_side(n, x, g, o, h, dt, B, T) for n, x, g, o, h in
+            (("q", q, gamma_q, q_out, cfg.num_q_heads), ("k", k, gamma_k, k_out, cfg.num_kv_heads))]
+    if positions is not None:
+        _i32("positions", positions, B * T)
+    _one_device(q, k, gamma_q, gamma_k, q_out, k_out, positions)
+    c = cfg.c()
+    (qr, qo), (kr, ko) = args
+    _check(lib().sas_qk_norm_rope(ctypes.byref(c), _ref(qr), _ref(kr), _ptr(gamma_q), _ptr(gamma_k), _ptr(positions),
+                                  B, T, rope_base, _ref(qo), _ref(ko), _stream(stream)), "sas_qk_norm_rope")
+
+
+def qk_norm_rope_workspace_bytes() -> int:
+    return int(lib().sas_qk_norm_rope_workspace_bytes())
+
+
+def qk_norm_rope_backward(cfg: Config, dq_out, dk_out, q, k, gamma_q, gamma_k, dq, dk, dgamma_q, dgamma_k,
+                          rope_base: float, ws, positions=None, stream=None) -> None:
+    """sas_qk_norm_rope_backward: writes dq / dk (may be dq_out / dk_out or
+    q / k) and adds to dgamma_q / dgamma_k (fp32 [128]); ws holds at least
+    qk_norm_rope_workspace_bytes() bytes."""
+    dt = kv_dtype(cfg)
+    B, T = _batch_tokens(q, k)
+    args = []
+    for n, x, g, o, d, dg, h in (("q", q, gamma_q, dq, dq_out, dgamma_q, cfg.num_q_heads),
+                                 ("k", k, gamma_k, dk, dk_out, dgamma_k, cfg.num_kv_heads)):
+        r, o_r = _norm_side(n, x, g, o, h, dt, B, T)
+        if (x is None) != (d is None) or (x is None) != (dg is None):
+            raise ValueError(f"d{n}_out and dgamma_{n} go with {n}: all of them or none")
+        if x is not None:
+            _plain(f"dgamma_{n}", dg, (128,), torch.float32)
+        args.append((r, o_r, None if d is None else _rows(f"d{n}_out", d, h, dt, B, T)))
+    if positions is not None:
+        _i32("positions", positions, B * T)
+    _one_device(q, k, gamma_q, gamma_k, dq, dk, dq_out, dk_out, dgamma_q, dgamma_k, positions, ws)
+    c = cfg.c()
+    (qr, qo, qd), (kr, ko, kd) = args
+    _check(lib().sas_qk_norm_rope_backward(ctypes.byref(c), _ref(qd), _ref(kd), _ref(qr), _ref(kr), _ptr(gamma_q),
+                                           _ptr(gamma_k), _ptr(positions), B, T, rope_base, _ref(qo), _ref(ko),
+                                           _ptr(dgamma_q), _ptr(dgamma_k), _ptr(ws), ws.nbytes, _stream(stream)),
+           "sas_qk_norm_rope_backward")
+
+
+def _batch_tokens(q, k):
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    if x.dim() != 4:
+        raise ValueError(f"[B][H][T][128] is wanted, got {tuple(x.shape)}")
+    return x.shape[0], x.shape[2]
+
+
+def _norm_side(name, x, gamma, out, heads, dtype, batch, tokens):
+    if x is None:
+        if out is not None:
+            raise ValueError(f"an output for {name} without {name}")
+        return None, None
+    if gamma is None or out is None:
+        raise ValueError(f"{name} needs its gain and its output")
+    _plain(f"gamma_{name}", gamma, (128,), torch.float32)
+    return _rows(name, x, heads, dtype, batch, tokens), _rows(f"{name} output", out, heads, dtype, batch, tokens)
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def kv8_append(cfg: Config, kv: KvCache8, k_new, v_new, ws, new_starts=None, new_lens=None,
+               max_new: Optional[int] = None, stream=None) -> None:
+    """sas_kv8_append: k_new / v_new bf16 [B][Hkv][T][128] (any strides), or
+    packed [1][Hkv][N][128] with new_starts int32 [B]; new_lens int32 [B] or
+    None (max_new tokens for every sequence); max_new defaults to T.
+    kv.seq_lens counts the new tokens in."""
+    B = kv.batch
+    packed = new_starts is not None
+    kr = _rows("k_new", k_new, cfg.num_kv_heads, torch.bfloat16, 1 if packed else B)
+    vr = _rows("v_new", v_new, cfg.num_kv_heads, torch.bfloat16, 1 if packed else B, int(k_new.shape[2]))
+    if packed:
+        kr.seq_stride = vr.seq_stride = 0
+        _i32("new_starts", new_starts, B)
+    if new_lens is not None:
+        _i32("new_lens", new_lens, B)
+    _one_device(k_new, v_new, new_starts, new_lens, ws, *kv.tensors())
+    c, c8 = cfg.c(), kv.c(cfg)
+    _check(lib().sas_kv8_append(ctypes.byref(c), ctypes.byref(c8), ctypes.byref(kr), ctypes.byref(vr),
+                                _ptr(new_starts), _ptr(new_lens), kr.tokens if max_new is None else max_new, _ptr(ws),
+                                ws.nbytes, _stream(stream)), "sas_kv8_append")
+
+
+def kv8_read(cfg: Config, kv: KvCache8, k_out, v_out, ws, begin=None, stream=None) -> None:
+    """sas_kv8_read: tokens begin[s] .. of every sequence into k_out / v_out
+    [B][Hkv][T][128] (cfg.out_dtype, any strides; either may be None)."""
+    outs = [None if t is None else _rows(n, t, cfg.num_kv_heads, out_dtype(cfg), kv.batch)
+            for n, t in (("k_out", k_out), ("v_out", v_out))]
+    counts = {r.tokens for r in outs if r is not None}
+    if len(counts) != 1:
+        raise ValueError("k_out and v_out must hold the same number of tokens, and one of them be given")
+    if begin is not None:
+        _i32("begin", begin, kv.batch)
+    _one_device(k_out, v_out, begin, ws, *kv.tensors())
+    c, c8 = cfg.c(), kv.c(cfg)
+    _check(lib().sas_kv8_read(ctypes.byref(c), ctypes.byref(c8), _ptr(begin), counts.pop(), _ref(outs[0]),
+                              _ref(outs[1]), _ptr(ws), ws.nbytes, _stream(stream)), "sas_kv8_read")
+
+
+def pool_keys_kv8(cfg: Config, kv: KvCache8, w_k, gamma_k, gate_keys, ws, blk_begin=None,
+                  num_blocks: Optional[int] = None, pooled_raw=None, stream=None) -> None:
+    """sas_pool_keys_kv8: pool_keys over an 8-bit cache."""
+    _check_gk(cfg, gate_keys)
+    B, hkv, mg = kv.batch, cfg.num_kv_heads, int(gate_keys.shape[2])
+    _plain("gate_keys", gate_keys, (B, hkv, mg, 128), gate_key_dtype(cfg))
+    _plain("w_k", w_k, (hkv, 384, 128), torch.bfloat16)
+    _plain("gamma_k", gamma_k, (128,), torch.float32)
+    if pooled_raw is not None:
+        _plain("pooled_raw", pooled_raw, (B, hkv, mg, 384), torch.float32)
+    if blk_begin is not None:
+        _i32("blk_begin", blk_begin, B)
+    _one_device(w_k, gamma_k, gate_keys, pooled_raw, blk_begin, ws, *kv.tensors())
+    c, c8 = cfg.c(), kv.c(cfg)
+    _check(lib().sas_pool_keys_kv8(ctypes.byref(c), ctypes.byref(c8), _ptr(blk_begin),
+                                   mg if num_blocks is None else int(num_blocks), _ptr(w_k), _ptr(gamma_k),
+                                   _ptr(gate_keys), mg, _ptr(pooled_raw), _ptr(ws), ws.nbytes, _stream(stream)),
+           "sas_pool_keys_kv8")
+
+
+def sparse_decode_kv8(cfg: Config, q, kv: KvCache8, sel_idx, sel_count, out, ws, stream=None) -> None:
+    """sas_sparse_decode_kv8: q bf16 [B][Hq][128], out cfg.out_dtype likewise;
+    sel_idx / sel_count as topk_blocks writes them, or both None: every block."""
+    B, hkv = kv.batch, cfg.num_kv_heads
+    _plain("q", q, (B, cfg.num_q_heads, 128), torch.bfloat16)
+    _plain("out", out, (B, cfg.num_q_heads, 128), out_dtype(cfg))
+    if (sel_idx is None) != (sel_count is None):
+        raise ValueError("sel_idx and sel_count: both or neither")
+    if sel_idx is not None:
+        _i32("sel_idx", sel_idx, B * hkv * cfg.max_sel)
+        _i32("sel_count", sel_count, B * hkv)
+    _one_device(q, out, sel_idx, sel_count, ws, *kv.tensors())
+    c, c8 = cfg.c(), kv.c(cfg)
+    _check(lib().sas_sparse_decode_kv8(ctypes.byref(c), _ptr(q), ctypes.byref(c8), _ptr(sel_idx), _ptr(sel_count),
+                                       _ptr(out), _ptr(ws), ws.nbytes, _stream(stream)), "sas_sparse_decode_kv8")
 
 
 def out_dtype(cfg: Config) -> torch.dtype:

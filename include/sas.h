@@ -445,6 +445,173 @@ SAS_API sas_status sas_decode_step_static(const sas_config* cfg, const void* q, 
                                           int32_t* sel_count, float* group_scores,
                                           uint32_t* status_out, sas_stream_t stream);
 
+/*
+ * ---- Norms of queries and keys with the position rotation ----
+ * The queries and keys that the entry points above read, made from the
+ * projections' output (Qwen3 layers: per-head RMSNorm, then rotary
+ * embedding).  The release pages have no counterpart.
+ */
+
+/* Rows of 128 contiguous elements of a [sequence][head][token] tensor with
+ * any strides, counted in elements: the row of (s, h, t) starts at
+ * data + s * seq_stride + h * head_stride + t * token_stride. */
+typedef struct {
+  void* data;           /* 16-byte aligned */
+  int64_t seq_stride;   /* strides >= 0, each a multiple of 16 bytes */
+  int64_t token_stride;
+  int64_t head_stride;
+  int64_t tokens;       /* token rows that data holds per sequence */
+} sas_rows;
+
+/*
+ * y = R(pos) (gamma * x / sqrt(mean(x^2) + eps)) of every query and key row,
+ * one gain for the query heads and one for the key heads; R rotates the pairs
+ * (i, i + 64) by pos * rope_base^(-2i/128).  Sums, the norm and the rotation
+ * run in fp32, the angle in fp64 up to its reduction (exact for any position);
+ * one rounding at the end.
+ *   cfg        num_q_heads, num_kv_heads, norm_eps and kv_dtype (bf16 or fp32,
+ *              of x and y) are used; rope_base is an argument, since
+ *              cfg->rope_base is the gate's
+ *   q, k       inputs [B][Hq][T] and [B][Hkv][T] rows; either may be NULL (and
+ *              its output with it): the other alone is computed
+ *   positions  int32 [B][T] on the device, or NULL: t.  A row whose position
+ *              is negative (padding) is skipped: its output stays as it was
+ *   q_out, k_out  may be the inputs themselves (same data and strides); any
+ *              other overlap, and rows of one output that overlap, are the
+ *              caller's error
+ */
+SAS_API sas_status sas_qk_norm_rope(const sas_config* cfg, const sas_rows* q, const sas_rows* k,
+                                    const float* gamma_q, const float* gamma_k,
+                                    const int32_t* positions, int32_t batch, int32_t seq_len,
+                                    float rope_base, const sas_rows* q_out, const sas_rows* k_out,
+                                    sas_stream_t stream);
+
+/* Bytes of workspace sas_qk_norm_rope_backward needs (any shape). */
+SAS_API size_t sas_qk_norm_rope_workspace_bytes(void);
+
+/*
+ * Gradient of sas_qk_norm_rope: for dq_out = dL/dq_out and dk_out = dL/dk_out
+ * (rows, kv_dtype), writes dq = dL/dq and dk = dL/dk (rows, kv_dtype; they may
+ * be dq_out and dk_out or q and k themselves) and ADDS to dgamma_q, dgamma_k
+ * (fp32 [128]; zero them first for a fresh gradient; fixed order of summation,
+ * repeated calls add identical values).  q, k are the forward's inputs.  Rows
+ * with a negative position are skipped and contribute nothing.  Queries or
+ * keys may be left out as in the forward (all of their pointers NULL).
+ *   ws  at least sas_qk_norm_rope_workspace_bytes() bytes, 16-byte aligned
+ */
+SAS_API sas_status sas_qk_norm_rope_backward(const sas_config* cfg, const sas_rows* dq_out,
+                                             const sas_rows* dk_out, const sas_rows* q,
+                                             const sas_rows* k, const float* gamma_q,
+                                             const float* gamma_k, const int32_t* positions,
+                                             int32_t batch, int32_t seq_len, float rope_base,
+                                             const sas_rows* dq, const sas_rows* dk,
+                                             float* dgamma_q, float* dgamma_k, void* ws,
+                                             size_t ws_bytes, sas_stream_t stream);
+
+/*
+ * ---- 8-bit KV cache ----
+ * Half the bytes of the bf16 cache.  Every block that precedes a sequence's
+ * current one is stored as 8-bit codes, keys and values each under one fp32
+ * scale per (block, KV head):
+ *   a = max(max |x| over the block's 64 x 128 values, 2^-100)
+ *   scale = a / qmax,  code = round-to-nearest-even(x * qmax / a)
+ * with qmax = 448 (e4m3) or 127 (int8); the stored value is code * scale.  A
+ * block that holds a NaN or an infinity gets scale NaN and codes 0: it reads
+ * back as NaN.  The current block -- the one of the last token, whether
+ * complete or not -- is kept in bf16 in the sequence's tail and is read from
+ * there.  A block is quantised once, when it completes, from its bf16 values:
+ * the cache's contents do not depend on how the tokens were split over calls.
+ * The release pages have no counterpart.
+ */
+typedef enum { SAS_KV8_E4M3 = 0, SAS_KV8_INT8 = 1 } sas_kv8_code;
+
+typedef struct {
+  void* k;                    /* key codes, 16-byte aligned: contiguous
+                                 [B][Hkv][capacity][128] or paged
+                                 [num_pages][Hkv][64][128] */
+  void* v;                    /* value codes, same layout */
+  float* k_scale;             /* [B][Hkv][capacity/64] or [num_pages][Hkv] */
+  float* v_scale;
+  void* k_tail;               /* bf16 [B][Hkv][64][128], 16-byte aligned: row
+                                 t % 64 holds token t of the current block */
+  void* v_tail;
+  const int32_t* block_table; /* NULL: contiguous; else [B][max_blocks_per_seq]
+                                 page ids (the current block needs one only
+                                 once it completes) */
+  const int32_t* seq_lens;    /* [B] tokens of each sequence, including those
+                                 that the call appends */
+  int32_t batch;              /* B >= 0 (0: nothing to do) */
+  int32_t capacity;           /* contiguous: tokens per (seq, head), multiple of 64 */
+  int32_t num_pages;
+  int32_t max_blocks_per_seq;
+  int32_t code;               /* sas_kv8_code */
+} sas_kv8;
+
+/*
+ * Append new tokens.  Sequence s gets n_s = new_lens[s] tokens (new_lens NULL:
+ * max_new each), positions seq_lens[s] - n_s .. seq_lens[s] - 1; blocks they
+ * complete are quantised into the cache, the current block's tokens go to the
+ * tail.  n_s = 0 leaves the sequence as it is, and tail rows past its length
+ * stay as they were.  Token i of sequence s is row new_starts[s] + i of
+ * (k_new, v_new) (new_starts NULL: row i): with seq_stride 0 and new_starts,
+ * the tokens of a ragged batch are packed one after another.
+ *   cfg           num_q_heads, num_kv_heads; kv_dtype must be bf16
+ *   k_new, v_new  bf16 rows [.][Hkv][tokens]
+ *   max_new       upper bound of every n_s (the launch is sized by it)
+ * A sequence with n_s outside 0 .. max_new, fewer than n_s tokens, rows past
+ * `tokens`, a length beyond the cache or a completed block's page out of
+ * range is skipped and reported as SAS_ERR_DEVICE_BOUNDS.  A page must not
+ * be written for two sequences in one call.
+ */
+SAS_API sas_status sas_kv8_append(const sas_config* cfg, const sas_kv8* kv, const sas_rows* k_new,
+                                  const sas_rows* v_new, const int32_t* new_starts,
+                                  const int32_t* new_lens, int32_t max_new, void* ws,
+                                  size_t ws_bytes, sas_stream_t stream);
+
+/*
+ * Read the cache back: row t of (k_out, v_out) gets token begin[s] + t of
+ * sequence s (begin NULL: 0) for t < count, as code * scale (fp32 product) or
+ * the tail's value, rounded to out_dtype.  Rows at or past the sequence's
+ * length stay as they were.  Either output may be NULL.  A token whose page is
+ * out of range reads as 0 and is reported as SAS_ERR_DEVICE_BOUNDS; a sequence
+ * with a length or begin out of range is skipped and reported.
+ *   cfg           num_kv_heads, out_dtype (bf16 or fp32, of the outputs)
+ *   k_out, v_out  rows [B][Hkv][count]
+ */
+SAS_API sas_status sas_kv8_read(const sas_config* cfg, const sas_kv8* kv, const int32_t* begin,
+                                int32_t count, const sas_rows* k_out, const sas_rows* v_out,
+                                void* ws, size_t ws_bytes, sas_stream_t stream);
+
+/*
+ * sas_pool_keys over the 8-bit cache: the pooled keys are those of the stored
+ * values (code * scale).  Same arguments and outputs; only complete blocks
+ * are pooled, the current one included when it is complete (its codes are
+ * written when it completes).
+ */
+SAS_API sas_status sas_pool_keys_kv8(const sas_config* cfg, const sas_kv8* kv,
+                                     const int32_t* blk_begin, int32_t num_blocks,
+                                     const void* w_k, const float* gamma_k, void* gate_keys,
+                                     int32_t max_gate_blocks, float* pooled_raw, void* ws,
+                                     size_t ws_bytes, sas_stream_t stream);
+
+/*
+ * sas_sparse_decode over the 8-bit cache: softmax attention of one query token
+ * per sequence over the listed blocks, the stored ones as code * scale and the
+ * current one from the tail.
+ *   q    bf16 [B][Hq][128] (16-byte aligned)
+ *   sel_idx [B][Hkv][budget/64], sel_count [B][Hkv]: as for sas_sparse_decode;
+ *        both NULL: every block of the sequence (dense attention, any length)
+ *   out  out_dtype [B][Hq][128]
+ * Logits, softmax statistics and sums are fp32.  The probabilities enter the
+ * product with the values as f16 (a bf16 output) or as the sum of two f16
+ * terms (an fp32 output).  kv_dtype must be bf16; the gated mode is refused
+ * as by sas_sparse_decode.
+ */
+SAS_API sas_status sas_sparse_decode_kv8(const sas_config* cfg, const void* q, const sas_kv8* kv,
+                                         const int32_t* sel_idx, const int32_t* sel_count,
+                                         void* out, void* ws, size_t ws_bytes,
+                                         sas_stream_t stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif
