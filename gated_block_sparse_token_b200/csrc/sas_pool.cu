@@ -215,8 +215,16 @@ cudaError_t prepare_pool_kernels() {
 }
 
 void fill_rope_table(RopeTable& t, float base) {
-  for (int i = 0; i < 64; ++i)
-    t.theta_over_pi[i] = std::pow(static_cast<double>(base), -2.0 * i / kDim) / M_PI;
+  // 64 powers cost a small kernel's launch: each host thread keeps the table
+  // of the last base it was asked for
+  thread_local float last_base = 0.f;  // no valid base
+  thread_local RopeTable last;
+  if (base != last_base) {
+    for (int i = 0; i < 64; ++i)
+      last.theta_over_pi[i] = std::pow(static_cast<double>(base), -2.0 * i / kDim) / M_PI;
+    last_base = base;
+  }
+  t = last;
 }
 
 // ---------------------------------------------------------------- tensor-core pooling and projection

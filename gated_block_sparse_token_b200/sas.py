@@ -187,6 +187,20 @@ class Config:
         return self.token_budget // 64
 
 
+_CONFIGS: dict = {}
+
+
+def _config(cfg: Config) -> _Config:
+    """cfg.c(), kept per content (a serving loop passes the same few)."""
+    key = tuple(cfg.__dict__.values())
+    c = _CONFIGS.get(key)
+    if c is None:
+        if len(_CONFIGS) >= 64:
+            _CONFIGS.clear()
+        c = _CONFIGS[key] = cfg.c()
+    return c
+
+
 @dataclass
 class KvCache:
     """Mirror of sas_kv holding the tensors alive.  block_table None: contiguous
@@ -211,13 +225,15 @@ class KvCache:
                    _ptr(self.token_budgets))
 
 
-@dataclass
+@dataclass(frozen=True)
 class KvCache8:
-    """Mirror of sas_kv8 holding the tensors alive.  The codes' dtype
+    """sas_kv8 holding the tensors alive.  The codes' dtype
     (torch.float8_e4m3fn or torch.int8) selects the code.  block_table None:
     codes [B][Hkv][capacity][128], scales [B][Hkv][capacity/64]; else paged
     codes [num_pages][Hkv][64][128], scales [num_pages][Hkv].  Tails are bf16
-    [B][Hkv][64][128] and hold each sequence's current block."""
+    [B][Hkv][64][128] and hold each sequence's current block.  Shapes, dtypes
+    and layouts are checked, and the C description taken, when the object is
+    made: change the tensors' contents freely, but not their storage."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor
@@ -227,21 +243,18 @@ class KvCache8:
     seq_lens: torch.Tensor
     block_table: Optional[torch.Tensor] = None
 
-    @property
-    def batch(self) -> int:
-        return int(self.seq_lens.shape[0])
-
-    def c(self, cfg: Config) -> _Kv8:
-        """The C description, after checking every shape, dtype and layout the
-        library takes from the configuration."""
-        hkv, B = cfg.num_kv_heads, self.seq_lens.shape[0]
-        k, v, bt = self.k, self.v, self.block_table
+    def __post_init__(self):
+        k, v, bt, lens = self.k, self.v, self.block_table, self.seq_lens
         code = _CODES.get(k.dtype)
         if code is None or v.dtype != k.dtype:
             raise ValueError(f"codes are {k.dtype} / {v.dtype}: both torch.float8_e4m3fn or both torch.int8 are wanted")
         ks = k.shape
-        if len(ks) != 4 or ks != v.shape or ks[1] != hkv or ks[3] != 128:
-            raise ValueError(f"codes are {tuple(ks)} / {tuple(v.shape)} for {hkv} KV heads")
+        if len(ks) != 4 or ks != v.shape or ks[3] != 128:
+            raise ValueError(f"codes are {tuple(ks)} / {tuple(v.shape)}")
+        if lens.dim() != 1:
+            raise ValueError(f"seq_lens is {tuple(lens.shape)}")
+        _i32("seq_lens", lens)
+        B, hkv = lens.shape[0], ks[1]
         if bt is None:
             if ks[0] != B or ks[2] % 64:
                 raise ValueError(f"contiguous codes are {tuple(ks)} for batch {B}")
@@ -257,46 +270,52 @@ class KvCache8:
         _plain("v_scale", self.v_scale, want, torch.float32)
         _plain("k_tail", self.k_tail, (B, hkv, 64, 128), torch.bfloat16)
         _plain("v_tail", self.v_tail, (B, hkv, 64, 128), torch.bfloat16)
-        _i32("seq_lens", self.seq_lens)
-        return _Kv8(k.data_ptr(), v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
-                    self.k_tail.data_ptr(), self.v_tail.data_ptr(), _ptr(bt), self.seq_lens.data_ptr(), B, cap, pages,
-                    width, code)
+        dev = k.get_device()
+        _on(dev, v, self.k_scale, self.v_scale, self.k_tail, self.v_tail, lens, bt)
+        c = _Kv8(k.data_ptr(), v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.k_tail.data_ptr(),
+                 self.v_tail.data_ptr(), _ptr(bt), lens.data_ptr(), B, cap, pages, width, code)
+        for name, value in (("batch", B), ("kv_heads", hkv), ("device", dev), ("_c", c)):
+            object.__setattr__(self, name, value)
 
-    def tensors(self):
-        return (self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail, self.seq_lens, self.block_table)
+    def c(self, cfg: Config) -> _Kv8:
+        if cfg.num_kv_heads != self.kv_heads:
+            raise ValueError(f"the cache has {self.kv_heads} KV heads, the config {cfg.num_kv_heads}")
+        return self._c
 
 
 def _plain(name: str, t, shape, dtype) -> None:
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}{'' if t.is_contiguous() else ' (strided)'}: "
                          f"contiguous {tuple(shape)} {dtype} is wanted")
 
 
 def _i32(name: str, t, n: Optional[int] = None) -> None:
-    if t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
+    if t.dtype is not torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
         raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}: contiguous int32"
                          + ("" if n is None else f" with {n} values") + " is wanted")
 
 
-def _rows(name: str, t, heads: int, dtype, batch: Optional[int] = None, tokens: Optional[int] = None) -> _Rows:
-    """sas_rows of a [B][H][T][128] tensor with any strides (last one 1)."""
-    sh = t.shape
-    if len(sh) != 4 or sh[1] != heads or sh[3] != 128 or t.dtype != dtype:
-        raise ValueError(f"{name} is {tuple(sh)} {t.dtype}: [B][{heads}][T][128] {dtype} is wanted")
-    if (batch is not None and sh[0] != batch) or (tokens is not None and sh[2] != tokens):
-        raise ValueError(f"{name} is {tuple(sh)}: batch {batch}, {tokens} tokens are wanted")
+def _rows(name: str, t, shape, dtype) -> _Rows:
+    """sas_rows of a tensor of shape [B][H][T][128] with any strides (last one 1)."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}: [B][H][T][128] = {tuple(shape)} {dtype} is wanted")
     st = t.stride()
     if st[3] != 1:
         raise ValueError(f"{name}: the 128 elements of a row must be contiguous")
-    return _Rows(t.data_ptr(), st[0], st[2], st[1], sh[2])
+    return _Rows(t.data_ptr(), st[0], st[2], st[1], shape[2])
 
 
-def _one_device(*tensors) -> None:
-    """Every tensor on the current CUDA device, where the library launches."""
-    dev = torch.cuda.current_device()
+def _on(dev: int, *tensors) -> None:
+    """Every tensor on CUDA device `dev`."""
     for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+            raise ValueError(f"a tensor is on {t.device}, cuda:{dev} is wanted")
+
+
+def _current(dev: int) -> None:
+    """The library launches on the current device."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on device {dev}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def abi_version() -> int:
@@ -465,13 +484,14 @@ def qk_norm_rope(cfg: Config, q, k, gamma_q, gamma_k, q_out, k_out, rope_base: f
     positions: int32 [B][T] (negative: the row is skipped) or None (0 .. T-1)."""
     dt = kv_dtype(cfg)
     B, T = _batch_tokens(q, k)
-    args = [_norm_side(n, x, g, o, h, dt, B, T) for n, x, g, o, h in
-            (("q", q, gamma_q, q_out, cfg.num_q_heads), ("k", k, gamma_k, k_out, cfg.num_kv_heads))]
+    qr, qo = _norm_side("q", q, gamma_q, q_out, cfg.num_q_heads, dt, B, T)
+    kr, ko = _norm_side("k", k, gamma_k, k_out, cfg.num_kv_heads, dt, B, T)
     if positions is not None:
         _i32("positions", positions, B * T)
-    _one_device(q, k, gamma_q, gamma_k, q_out, k_out, positions)
-    c = cfg.c()
-    (qr, qo), (kr, ko) = args
+    dev = (q if q is not None else k).get_device()
+    _current(dev)
+    _on(dev, q, k, gamma_q, gamma_k, q_out, k_out, positions)
+    c = _config(cfg)
     _check(lib().sas_qk_norm_rope(ctypes.byref(c), _ref(qr), _ref(kr), _ptr(gamma_q), _ptr(gamma_k), _ptr(positions),
                                   B, T, rope_base, _ref(qo), _ref(ko), _stream(stream)), "sas_qk_norm_rope")
 
@@ -495,11 +515,13 @@ def qk_norm_rope_backward(cfg: Config, dq_out, dk_out, q, k, gamma_q, gamma_k, d
             raise ValueError(f"d{n}_out and dgamma_{n} go with {n}: all of them or none")
         if x is not None:
             _plain(f"dgamma_{n}", dg, (128,), torch.float32)
-        args.append((r, o_r, None if d is None else _rows(f"d{n}_out", d, h, dt, B, T)))
+        args.append((r, o_r, None if d is None else _rows(f"d{n}_out", d, (B, h, T, 128), dt)))
     if positions is not None:
         _i32("positions", positions, B * T)
-    _one_device(q, k, gamma_q, gamma_k, dq, dk, dq_out, dk_out, dgamma_q, dgamma_k, positions, ws)
-    c = cfg.c()
+    dev = ws.get_device()
+    _current(dev)
+    _on(dev, q, k, gamma_q, gamma_k, dq, dk, dq_out, dk_out, dgamma_q, dgamma_k, positions)
+    c = _config(cfg)
     (qr, qo, qd), (kr, ko, kd) = args
     _check(lib().sas_qk_norm_rope_backward(ctypes.byref(c), _ref(qd), _ref(kd), _ref(qr), _ref(kr), _ptr(gamma_q),
                                            _ptr(gamma_k), _ptr(positions), B, T, rope_base, _ref(qo), _ref(ko),
@@ -511,9 +533,10 @@ def _batch_tokens(q, k):
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
-    if x.dim() != 4:
-        raise ValueError(f"[B][H][T][128] is wanted, got {tuple(x.shape)}")
-    return x.shape[0], x.shape[2]
+    sh = x.shape
+    if len(sh) != 4:
+        raise ValueError(f"[B][H][T][128] is wanted, got {tuple(sh)}")
+    return sh[0], sh[2]
 
 
 def _norm_side(name, x, gamma, out, heads, dtype, batch, tokens):
@@ -523,8 +546,9 @@ def _norm_side(name, x, gamma, out, heads, dtype, batch, tokens):
         return None, None
     if gamma is None or out is None:
         raise ValueError(f"{name} needs its gain and its output")
-    _plain(f"gamma_{name}", gamma, (128,), torch.float32)
-    return _rows(name, x, heads, dtype, batch, tokens), _rows(f"{name} output", out, heads, dtype, batch, tokens)
+    shape = (batch, heads, tokens, 128)
+    _plain("its gain", gamma, (128,), torch.float32)
+    return _rows(name, x, shape, dtype), _rows("its output", out, shape, dtype)
 
 
 def _ref(s):
@@ -539,15 +563,19 @@ def kv8_append(cfg: Config, kv: KvCache8, k_new, v_new, ws, new_starts=None, new
     kv.seq_lens counts the new tokens in."""
     B = kv.batch
     packed = new_starts is not None
-    kr = _rows("k_new", k_new, cfg.num_kv_heads, torch.bfloat16, 1 if packed else B)
-    vr = _rows("v_new", v_new, cfg.num_kv_heads, torch.bfloat16, 1 if packed else B, int(k_new.shape[2]))
+    if k_new.dim() != 4:
+        raise ValueError(f"k_new is {tuple(k_new.shape)}: [B][H][T][128] is wanted")
+    shape = (1 if packed else B, cfg.num_kv_heads, k_new.shape[2], 128)
+    kr = _rows("k_new", k_new, shape, torch.bfloat16)
+    vr = _rows("v_new", v_new, shape, torch.bfloat16)
     if packed:
         kr.seq_stride = vr.seq_stride = 0
         _i32("new_starts", new_starts, B)
     if new_lens is not None:
         _i32("new_lens", new_lens, B)
-    _one_device(k_new, v_new, new_starts, new_lens, ws, *kv.tensors())
-    c, c8 = cfg.c(), kv.c(cfg)
+    _current(kv.device)
+    _on(kv.device, k_new, v_new, new_starts, new_lens, ws)
+    c, c8 = _config(cfg), kv.c(cfg)
     _check(lib().sas_kv8_append(ctypes.byref(c), ctypes.byref(c8), ctypes.byref(kr), ctypes.byref(vr),
                                 _ptr(new_starts), _ptr(new_lens), kr.tokens if max_new is None else max_new, _ptr(ws),
                                 ws.nbytes, _stream(stream)), "sas_kv8_append")
@@ -556,17 +584,19 @@ def kv8_append(cfg: Config, kv: KvCache8, k_new, v_new, ws, new_starts=None, new
 def kv8_read(cfg: Config, kv: KvCache8, k_out, v_out, ws, begin=None, stream=None) -> None:
     """sas_kv8_read: tokens begin[s] .. of every sequence into k_out / v_out
     [B][Hkv][T][128] (cfg.out_dtype, any strides; either may be None)."""
-    outs = [None if t is None else _rows(n, t, cfg.num_kv_heads, out_dtype(cfg), kv.batch)
-            for n, t in (("k_out", k_out), ("v_out", v_out))]
-    counts = {r.tokens for r in outs if r is not None}
-    if len(counts) != 1:
-        raise ValueError("k_out and v_out must hold the same number of tokens, and one of them be given")
+    x = k_out if k_out is not None else v_out
+    if x is None or x.dim() != 4:
+        raise ValueError("k_out or v_out [B][H][T][128] is wanted")
+    shape, dt = (kv.batch, cfg.num_kv_heads, x.shape[2], 128), out_dtype(cfg)
+    kr = None if k_out is None else _rows("k_out", k_out, shape, dt)
+    vr = None if v_out is None else _rows("v_out", v_out, shape, dt)
     if begin is not None:
         _i32("begin", begin, kv.batch)
-    _one_device(k_out, v_out, begin, ws, *kv.tensors())
-    c, c8 = cfg.c(), kv.c(cfg)
-    _check(lib().sas_kv8_read(ctypes.byref(c), ctypes.byref(c8), _ptr(begin), counts.pop(), _ref(outs[0]),
-                              _ref(outs[1]), _ptr(ws), ws.nbytes, _stream(stream)), "sas_kv8_read")
+    _current(kv.device)
+    _on(kv.device, k_out, v_out, begin, ws)
+    c, c8 = _config(cfg), kv.c(cfg)
+    _check(lib().sas_kv8_read(ctypes.byref(c), ctypes.byref(c8), _ptr(begin), shape[2], _ref(kr), _ref(vr),
+                              _ptr(ws), ws.nbytes, _stream(stream)), "sas_kv8_read")
 
 
 def pool_keys_kv8(cfg: Config, kv: KvCache8, w_k, gamma_k, gate_keys, ws, blk_begin=None,
@@ -581,8 +611,9 @@ def pool_keys_kv8(cfg: Config, kv: KvCache8, w_k, gamma_k, gate_keys, ws, blk_be
         _plain("pooled_raw", pooled_raw, (B, hkv, mg, 384), torch.float32)
     if blk_begin is not None:
         _i32("blk_begin", blk_begin, B)
-    _one_device(w_k, gamma_k, gate_keys, pooled_raw, blk_begin, ws, *kv.tensors())
-    c, c8 = cfg.c(), kv.c(cfg)
+    _current(kv.device)
+    _on(kv.device, w_k, gamma_k, gate_keys, pooled_raw, blk_begin, ws)
+    c, c8 = _config(cfg), kv.c(cfg)
     _check(lib().sas_pool_keys_kv8(ctypes.byref(c), ctypes.byref(c8), _ptr(blk_begin),
                                    mg if num_blocks is None else int(num_blocks), _ptr(w_k), _ptr(gamma_k),
                                    _ptr(gate_keys), mg, _ptr(pooled_raw), _ptr(ws), ws.nbytes, _stream(stream)),
@@ -600,8 +631,9 @@ def sparse_decode_kv8(cfg: Config, q, kv: KvCache8, sel_idx, sel_count, out, ws,
     if sel_idx is not None:
         _i32("sel_idx", sel_idx, B * hkv * cfg.max_sel)
         _i32("sel_count", sel_count, B * hkv)
-    _one_device(q, out, sel_idx, sel_count, ws, *kv.tensors())
-    c, c8 = cfg.c(), kv.c(cfg)
+    _current(kv.device)
+    _on(kv.device, q, out, sel_idx, sel_count, ws)
+    c, c8 = _config(cfg), kv.c(cfg)
     _check(lib().sas_sparse_decode_kv8(ctypes.byref(c), _ptr(q), ctypes.byref(c8), _ptr(sel_idx), _ptr(sel_count),
                                        _ptr(out), _ptr(ws), ws.nbytes, _stream(stream)), "sas_sparse_decode_kv8")
 
