@@ -16,6 +16,7 @@ cudaError_t prepare_pool_kernels();
 cudaError_t prepare_prefill_kernels();
 cudaError_t prepare_backward_kernels();
 cudaError_t prepare_prefill_backward_kernels();
+cudaError_t prepare_kv8_kernels();
 }
 
 namespace {
@@ -38,6 +39,11 @@ std::once_flag g_once;
 cudaError_t g_prep_err = cudaSuccess;
 EncodeTiledFn g_encode = nullptr;
 
+// Kernel attributes are per device: set them on the first call of each.
+constexpr int kMaxDevices = 64;
+std::once_flag g_dev_once[kMaxDevices];
+cudaError_t g_dev_err[kMaxDevices] = {};
+
 cudaError_t prepare() {
   std::call_once(g_once, [] {
     void* fn = nullptr;
@@ -49,13 +55,22 @@ cudaError_t prepare() {
       return;
     }
     g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-    g_prep_err = sas::prepare_decode_kernels();
-    if (g_prep_err == cudaSuccess) g_prep_err = sas::prepare_pool_kernels();
-    if (g_prep_err == cudaSuccess) g_prep_err = sas::prepare_prefill_kernels();
-    if (g_prep_err == cudaSuccess) g_prep_err = sas::prepare_backward_kernels();
-    if (g_prep_err == cudaSuccess) g_prep_err = sas::prepare_prefill_backward_kernels();
   });
-  return g_prep_err;
+  if (g_prep_err != cudaSuccess) return g_prep_err;
+  int dev = -1;
+  const cudaError_t ed = cudaGetDevice(&dev);
+  if (ed != cudaSuccess) return ed;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::call_once(g_dev_once[dev], [dev] {
+    cudaError_t e = sas::prepare_decode_kernels();
+    if (e == cudaSuccess) e = sas::prepare_pool_kernels();
+    if (e == cudaSuccess) e = sas::prepare_prefill_kernels();
+    if (e == cudaSuccess) e = sas::prepare_backward_kernels();
+    if (e == cudaSuccess) e = sas::prepare_prefill_backward_kernels();
+    if (e == cudaSuccess) e = sas::prepare_kv8_kernels();
+    g_dev_err[dev] = e;
+  });
+  return g_dev_err[dev];
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -967,6 +982,12 @@ sas_status sas_qk_norm_rope_backward(const sas_config* cfg, const sas_rows* dq_o
 // ---------------------------------------------------------------- 8-bit cache
 namespace {
 
+// 64-token tiles (one block of one KV head) of the cache.
+long long kv8_tiles(const sas_config* cfg, const sas_kv8* kv) {
+  return kv->block_table != nullptr ? static_cast<long long>(kv->num_pages) * cfg->num_kv_heads
+                                    : static_cast<long long>(kv->batch) * cfg->num_kv_heads * (kv->capacity / 64);
+}
+
 // Checks every 8-bit cache call makes.  The caller handles batch 0.
 sas_status check_kv8(const sas_config* cfg, const sas_kv8* kv, const void* ws, size_t ws_bytes) {
   sas_status st = check_config(cfg);
@@ -987,6 +1008,8 @@ sas_status check_kv8(const sas_config* cfg, const sas_kv8* kv, const void* ws, s
     if (kv->capacity < 64 || kv->capacity % 64 != 0) return SAS_ERR_INVALID_ARG;
   }
   if (static_cast<long long>(kv->batch) * cfg->num_kv_heads > 65535) return SAS_ERR_UNSUPPORTED;
+  // tile numbers are int32
+  if (kv8_tiles(cfg, kv) > 0x7fffffffLL) return SAS_ERR_UNSUPPORTED;
   return SAS_OK;
 }
 
@@ -1116,6 +1139,7 @@ sas_status sas_sparse_decode_kv8(const sas_config* cfg, const void* q, const sas
   p.sel_count = sel_count;
   p.out = out;
   p.status = static_cast<uint32_t*>(ws);
+  if (prepare() != cudaSuccess) return SAS_ERR_CUDA;
   return launch_result(sas::launch_kv8_attend(kv->code, cfg->out_dtype == SAS_DTYPE_F32, p, kv->batch,
                                               reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -223,9 +223,14 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ K
 // out_g = sum_j softmax_j(q_g . k_j * scale) v_j over the tokens of the listed
 // blocks (or of every block), one cluster of CTAs per (sequence, KV head).
 //
-// Bound by memory: 16 KiB of codes a block.  Each warp takes 16 keys of a
-// block straight from global memory into registers (no shared memory, no
-// barrier in the loop), the next block's loads in flight while one is used:
+// Bound by memory: 16 KiB of codes a block.  A group of four warps takes whole
+// blocks, 16 keys a warp; a CTA holds one group or two.  Every warp streams
+// its own 4 KiB slices through its own ring of kKaStages slots (cp.async, 16
+// bytes a lane): the loop has no barrier and no producer, and tens of KiB are in
+// flight on every SM whatever the register use.  (Loads into registers, one
+// slice ahead, left too little in flight: 84 us for 32 ragged sequences of
+// 4,096 listed tokens against 59; a ring fed by 2-D TMA from a lane of one of
+// the consuming warps cost that warp the issue of two copies a block.)
 //   S^T = K q^T  m16n8k16 f16: the 16 keys are the rows, the (up to 8) heads
 //                of the group the columns; codes are exact in f16, and the
 //                query is scaled by a power of two per head into f16's range
@@ -239,13 +244,18 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ K
 //                fp32 output a second product carries the remainder.  The sum
 //                runs over the unrounded p.
 // Both products take their k index from whatever order makes a lane's 16-byte
-// load its fragment: dims 16t .. 16t+15 and 64 + those for K, dims 16g .. of
-// four keys for V.  The block's two scales enter as fp32 factors of S and O.
+// shared load its fragment: dims 16t .. 16t+15 and 64 + those for K, dims 16g ..
+// of four keys for V.  Key g of a fragment is row 2(g/2) + g/4 (xor 4 for odd
+// g) of its eight: with the swizzle both operands' loads are then free of bank
+// conflicts.  The block's two scales enter as fp32 factors of S and O.
 // The current block comes from the bf16 tail on bf16 products (P as a sum of
-// two bf16 terms), rows past the length masked.
-constexpr int kKaWarps = 4;
+// two bf16 terms), rows past the length masked, while the ring first fills.
+constexpr int kKaStages = 3;                       // ring slots of a warp
+constexpr int kKaSlot = 2 * 16 * kDim;             // 16 rows of K, then of V
 constexpr int kKaHeadPair = 2 * kDim + 4;  // floats between head pairs of a partial (bank spread)
 constexpr int kKaPart = (kMaxGroup / 2) * kKaHeadPair;
+constexpr int kKaMaxWarps = 8;
+constexpr int kKaMaxCluster = 16;  // beyond the portable 8: allowed by an attribute
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -261,11 +271,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return r;
 }
 
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
   return r;
 }
 
@@ -274,11 +291,6 @@ __device__ __forceinline__ float ld_dsmem(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-
-struct KaFrag {
-  uint4 k[4];  // rows g, g + 8: dims 16t.., 64 + 16t..
-  uint4 v[4];  // keys 2t, 2t + 1, 2t + 8, 2t + 9: dims 16g..
-};
 
 struct KaState {
   float m[2], l[2];   // heads 2t, 2t + 1 (m in the base-2 logit domain, uniform over g)
@@ -310,28 +322,35 @@ __device__ __forceinline__ void raise_max(KaState& st, const float (&sc)[4]) {
   }
 }
 
-// One 16-key slice of a stored block.
+// One 16-key slice of a stored block: rows at ks_addr and vs_addr in shared
+// memory, swizzled in 16-byte units by their row modulo 8.  kr: the K row of
+// this lane (key g), vr: the V rows of keys 2t and 2t + 1 (row 8 further: keys
+// g + 8, ...).
 template <int CODE, bool SPLIT>
-__device__ __forceinline__ void attend_codes(KaState& st, const KaFrag& f, const uint32_t (&qf)[16],
-                                             const float (&qs)[2], float ks, float vs) {
-  float sc[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint32_t vs_addr,
+                                             const uint32_t (&qf)[16], const float (&qs)[2], float ks, float vs) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int kr = (2 * (g >> 1) + (g >> 2)) ^ (4 * (g & 1)), vr = 2 * t + (t >> 1);
+  float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    const uint32_t r0[4] = {f.k[2 * c].x, f.k[2 * c].y, f.k[2 * c].z, f.k[2 * c].w};
-    const uint32_t r1[4] = {f.k[2 * c + 1].x, f.k[2 * c + 1].y, f.k[2 * c + 1].z, f.k[2 * c + 1].w};
+    const uint32_t at = ks_addr + kr * kDim + (((t + 4 * c) ^ kr) << 4);
+    const uint4 x0 = lds128(at), x1 = lds128(at + 8 * kDim);
+    const uint32_t r0[4] = {x0.x, x0.y, x0.z, x0.w};
+    const uint32_t r1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t a0, a1, a2, a3;
       codes_f16<CODE>(r0[j], a0, a2);
       codes_f16<CODE>(r1[j], a1, a3);
-      mma_f16(sc, a0, a1, a2, a3, qf[8 * c + 2 * j], qf[8 * c + 2 * j + 1]);
+      mma_f16(c == 0 ? sc : sd, a0, a1, a2, a3, qf[8 * c + 2 * j], qf[8 * c + 2 * j + 1]);
     }
   }
   const float f0 = qs[0] * ks, f1 = qs[1] * ks;
-  sc[0] *= f0;
-  sc[1] *= f1;
-  sc[2] *= f0;
-  sc[3] *= f1;
+  sc[0] = (sc[0] + sd[0]) * f0;
+  sc[1] = (sc[1] + sd[1]) * f1;
+  sc[2] = (sc[2] + sd[2]) * f0;
+  sc[3] = (sc[3] + sd[3]) * f1;
   raise_max(st, sc);
   float p[4];
 #pragma unroll
@@ -345,10 +364,10 @@ __device__ __forceinline__ void attend_codes(KaState& st, const KaFrag& f, const
     e0 = transpose8x8(pack_f16x2(p[0] - f16_lo(h0), p[1] - f16_hi(h0)));
     e1 = transpose8x8(pack_f16x2(p[2] - f16_lo(h1), p[3] - f16_hi(h1)));
   }
-  const uint32_t va[4] = {f.v[0].x, f.v[0].y, f.v[0].z, f.v[0].w};
-  const uint32_t vb[4] = {f.v[1].x, f.v[1].y, f.v[1].z, f.v[1].w};
-  const uint32_t vc[4] = {f.v[2].x, f.v[2].y, f.v[2].z, f.v[2].w};
-  const uint32_t vd[4] = {f.v[3].x, f.v[3].y, f.v[3].z, f.v[3].w};
+  const uint32_t at0 = vs_addr + vr * kDim + ((g ^ vr) << 4), at1 = vs_addr + (vr ^ 4) * kDim + ((g ^ vr ^ 4) << 4);
+  const uint4 y0 = lds128(at0), y1 = lds128(at1), y2 = lds128(at0 + 8 * kDim), y3 = lds128(at1 + 8 * kDim);
+  const uint32_t va[4] = {y0.x, y0.y, y0.z, y0.w}, vb[4] = {y1.x, y1.y, y1.z, y1.w};
+  const uint32_t vc[4] = {y2.x, y2.y, y2.z, y2.w}, vd[4] = {y3.x, y3.y, y3.z, y3.w};
 #pragma unroll
   for (int w = 0; w < 2; ++w) {  // dims 4w .. 4w + 3 and 8 + those of the lane's 16
 #pragma unroll
@@ -433,46 +452,106 @@ __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt
 }  // namespace
 
 template <int CODE, bool F32OUT>
-__global__ void __launch_bounds__(32 * kKaWarps) kv8_attend_kernel(const __grid_constant__ Kv8AttendParams p) {
-  __shared__ __align__(16) float part[kKaWarps][kKaPart];
-  __shared__ float ml[kKaWarps][2][kMaxGroup];
+__global__ void __launch_bounds__(256, 2)
+    kv8_attend_kernel(const __grid_constant__ Kv8AttendParams p) {
+  // the warps' rings; once every block is used, the warps' partials
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  float* part = reinterpret_cast<float*>(smem_raw);
+  __shared__ float ml[kKaMaxWarps][2][kMaxGroup];
   __shared__ float cta_ml[2][kMaxGroup];
   __shared__ int cta_bad;
   const int CS = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);
   const int pair = static_cast<int>(blockIdx.y);
   const int s = pair / p.kv.hkv, h = pair - s * p.kv.hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int threads = static_cast<int>(blockDim.x), n_warps = threads >> 5;
   const int G = p.G;
+  // this warp's group among all of the cluster's
+  const int NG = CS * (n_warps >> 2), grp = rank * (n_warps >> 2) + (warp >> 2), quarter = warp & 3;
   griddep_launch_dependents();
   griddep_wait();
 
-  // ---- the list
+  // ---- the list.  Entries grp, grp + NG, .. below m - 1 are this group's
+  // stored blocks; lane l holds block, tile and scales of a chunk's l-th.  The
+  // first chunk's block numbers are read together with the length and the count
+  // (inside the list's storage whatever those turn out to be).
+  const int32_t* sel = p.sel_idx != nullptr ? p.sel_idx + static_cast<size_t>(pair) * p.max_sel : nullptr;
   const int L = p.kv.seq_lens[s];
+  int m = 0, first_b = 0, first_next = 0, last_b = 0;
+  const int first_j = grp + NG * lane;
+  if (sel != nullptr) {
+    m = p.sel_count[pair];
+    if (first_j < p.max_sel) first_b = sel[first_j];
+    if (first_j + 1 < p.max_sel) first_next = sel[first_j + 1];
+  }
+  const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(s) * p.hq + static_cast<size_t>(h) * G + min(g, G - 1)) * kDim;
+  uint32_t raw[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 x = *reinterpret_cast<const uint4*>(qrow + 64 * (i >> 1) + 16 * t + 8 * (i & 1));
+    raw[4 * i] = x.x, raw[4 * i + 1] = x.y, raw[4 * i + 2] = x.z, raw[4 * i + 3] = x.w;
+  }
   bool bad = L < 1 || static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
   const int c = bad ? 0 : (L - 1) / kBlock;
-  int m = c + 1;
-  const int32_t* sel = nullptr;
-  if (p.sel_idx != nullptr) {
-    m = p.sel_count[pair];
-    sel = p.sel_idx + static_cast<size_t>(pair) * p.max_sel;
+  if (sel == nullptr) {
+    m = c + 1;
+  } else {
     if (m < 1 || m > p.max_sel) bad = true;
-    if (!bad && sel[m - 1] != c) bad = true;
+    if (!bad) last_b = sel[m - 1];
   }
-  // stored blocks of this CTA: entries rank, rank + CS, .. below m - 1; warp w
-  // takes keys 16w .. 16w + 15 of each
-  const int n = bad || rank >= m - 1 ? 0 : (m - 2 - rank) / CS + 1;
+  int n = bad || grp >= m - 1 ? 0 : (m - 2 - grp) / NG + 1;
+
+  int tile_c = 0, tile_n = 0;
+  float ks_c = 0.f, vs_c = 0.f, ks_n = 0.f, vs_n = 0.f;
+  auto fetch = [&](int i0, int& tile, float& ks, float& vs) -> bool {  // entries i0 .. i0 + 31
+    const int i = i0 + lane;
+    bool ok = true;
+    tile = 0;
+    if (i < n) {
+      const int j = grp + NG * i;
+      const int b = sel == nullptr ? j : (i0 == 0 ? first_b : sel[j]);
+      if (sel != nullptr && (i0 == 0 ? first_next : sel[j + 1]) <= b) ok = false;  // ascending, so all lie below c
+      const long long at = b < c ? p.kv.tile(s, h, b) : -1;
+      if (at < 0) ok = false;
+      if (ok) {
+        tile = static_cast<int>(at);
+        ks = p.kv.k_scale[tile];
+        vs = p.kv.v_scale[tile];
+      }
+    }
+    return __all_sync(0xffffffffu, ok);
+  };
+  if (n > 0 && !fetch(0, tile_c, ks_c, vs_c)) {
+    bad = true;
+    n = 0;
+  }
+  // lane: 16-byte unit lane % 8 of rows lane / 8 + 4k, stored at that unit xor
+  // the row modulo 8
+  const uint32_t ring = smem_u32(smem_raw) + warp * (kKaStages * kKaSlot);
+  const uint32_t d_even = (lane >> 3) * kDim + (((lane & 7) ^ (lane >> 3)) << 4);
+  const uint32_t d_odd = d_even ^ 64u;  // rows 4 further: the unit xor 4
+  const size_t src_off = static_cast<size_t>(quarter) * (16 * kDim) + 16 * lane;
+  auto issue = [&](uint32_t slot, int tile) {
+    const uint8_t* kp = p.kv.k + static_cast<size_t>(tile) * kTile8Bytes + src_off;
+    const uint8_t* vp = p.kv.v + static_cast<size_t>(tile) * kTile8Bytes + src_off;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t dst = slot + 4 * k * kDim + ((k & 1) ? d_odd : d_even);
+      cp_async16(dst, kp + 4 * k * kDim);
+      cp_async16(dst + 16 * kDim, vp + 4 * k * kDim);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kKaStages; ++i) {
+    const int tile = __shfl_sync(0xffffffffu, tile_c, i);
+    if (i < n) issue(ring + i * kKaSlot, tile);
+    cp_async_commit();
+  }
 
   // ---- the query, as B fragments: head g, dims 16t .. and 64 + 16t ..
   uint32_t qf[16];
   float qs[2];
-  const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(s) * p.hq + static_cast<size_t>(h) * G + min(g, G - 1)) * kDim;
   {
-    uint32_t raw[16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(qrow + 64 * (i >> 1) + 16 * t + 8 * (i & 1));
-      raw[4 * i] = x.x, raw[4 * i + 1] = x.y, raw[4 * i + 2] = x.z, raw[4 * i + 3] = x.w;
-    }
     uint32_t mag = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -482,7 +561,7 @@ __global__ void __launch_bounds__(32 * kKaWarps) kv8_attend_kernel(const __grid_
     mag = max(mag & 0xffffu, mag >> 16);
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-    // biased exponent e of the largest value (1 .. 254): q 2^(127-e) lies in [0, 2)
+    // biased exponent e of the largest value (1 .. 253): q 2^(127-e) lies in [0, 4)
     const uint32_t e = min(max(mag >> 7, 1u), 253u);
     const float dn = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
 #pragma unroll
@@ -502,76 +581,38 @@ __global__ void __launch_bounds__(32 * kKaWarps) kv8_attend_kernel(const __grid_
 #pragma unroll
     for (int e = 0; e < 4; ++e) st.acc[j][e] = 0.f;
 
-  // ---- stored blocks.  Lane l holds the tile and scales of the chunk's l-th
-  // entry; a tile out of range ends the warp's loop.
-  long long tile_c = 0, tile_n = 0;
-  float ks_c = 0.f, vs_c = 0.f, ks_n = 0.f, vs_n = 0.f;
-  auto fetch = [&](int i0, long long& tile, float& ks, float& vs) -> bool {  // entries i0 .. i0 + 31
-    const int i = i0 + lane;
-    bool ok = true;
-    tile = 0;
-    if (i < n) {
-      const int j = rank + CS * i;
-      const int b = sel != nullptr ? sel[j] : j;
-      if (sel != nullptr && sel[j + 1] <= b) ok = false;  // ascending, so every block is below c
-      tile = b < c ? p.kv.tile(s, h, b) : -1;
-      if (tile < 0) {
-        ok = false;
-        tile = 0;
-      }
-      if (ok) {
-        ks = p.kv.k_scale[tile];
-        vs = p.kv.v_scale[tile];
-      }
-    }
-    return __all_sync(0xffffffffu, ok);
-  };
-  auto load = [&](KaFrag& f, long long tile) {
-    const uint8_t* kp = p.kv.k + tile * kTile8Bytes + (16 * warp + g) * kDim + 16 * t;
-    f.k[0] = ld_stream(kp);
-    f.k[1] = ld_stream(kp + 8 * kDim);
-    f.k[2] = ld_stream(kp + 64);
-    f.k[3] = ld_stream(kp + 8 * kDim + 64);
-    const uint8_t* vp = p.kv.v + tile * kTile8Bytes + (16 * warp + 2 * t) * kDim + 16 * g;
-    f.v[0] = ld_stream(vp);
-    f.v[1] = ld_stream(vp + kDim);
-    f.v[2] = ld_stream(vp + 8 * kDim);
-    f.v[3] = ld_stream(vp + 9 * kDim);
-  };
-  int n_ok = n;  // entries whose tiles are known to be in range
-  if (n > 0) {
-    if (!fetch(0, tile_c, ks_c, vs_c)) {
-      bad = true;
-      n_ok = 0;
-    }
-  }
-  if (n_ok > 0) {
-    KaFrag f0, f1;
-    load(f0, __shfl_sync(0xffffffffu, tile_c, 0));
-    auto step = [&](int i, KaFrag& cur, KaFrag& nxt) {
-      if ((i & 31) == 0 && i + 32 < n_ok && !fetch(i + 32, tile_n, ks_n, vs_n)) {
-        bad = true;
-        n_ok = i + 32;
-      }
-      if (i + 1 < n_ok) load(nxt, __shfl_sync(0xffffffffu, (i & 31) == 31 ? tile_n : tile_c, (i + 1) & 31));
-      attend_codes<CODE, F32OUT>(st, cur, qf, qs, __shfl_sync(0xffffffffu, ks_c, i & 31),
-                                 __shfl_sync(0xffffffffu, vs_c, i & 31));
-      if ((i & 31) == 31) {
-        tile_c = tile_n;
-        ks_c = ks_n;
-        vs_c = vs_n;
-      }
-    };
-    for (int i = 0; i < n_ok; i += 2) {
-      step(i, f0, f1);
-      if (i + 1 < n_ok) step(i + 1, f1, f0);
-    }
-  }
-  // ---- the current block: the CTA whose turn it is
-  if (!bad && rank == (m - 1) % CS && 16 * warp < L - c * kBlock) {
+  // ---- the current block: the group whose turn it is, while its ring fills
+  if (sel != nullptr && last_b != c) bad = true;
+  if (!bad && grp == (m - 1) % NG && 16 * quarter < L - c * kBlock) {
     const size_t off = static_cast<size_t>(pair) * (kBlock * kDim);
-    attend_tail(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * warp, L - c * kBlock, p.scale_log2);
+    attend_tail(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * quarter, L - c * kBlock, p.scale_log2);
   }
+
+  // ---- the stored blocks
+  uint32_t slot = ring;
+  for (int i = 0; i < n; ++i) {
+    if ((i & 31) == 0 && i + 32 < n && !fetch(i + 32, tile_n, ks_n, vs_n)) {
+      bad = true;
+      n = i + 32;
+    }
+    cp_async_wait<kKaStages - 1>();
+    __syncwarp();
+    attend_codes<CODE, F32OUT>(st, slot, slot + 16 * kDim, qf, qs, __shfl_sync(0xffffffffu, ks_c, i & 31),
+                               __shfl_sync(0xffffffffu, vs_c, i & 31));
+    __syncwarp();
+    const int nxt = i + kKaStages;  // into the slot just used
+    const int tile = __shfl_sync(0xffffffffu, ((i ^ nxt) & ~31) ? tile_n : tile_c, nxt & 31);
+    if (nxt < n) issue(slot, tile);
+    cp_async_commit();
+    if ((i & 31) == 31) {
+      tile_c = tile_n;
+      ks_c = ks_n;
+      vs_c = vs_n;
+    }
+    slot += kKaSlot;
+    if (slot == ring + kKaStages * kKaSlot) slot = ring;
+  }
+  __syncthreads();  // every copy has landed and been used: the rings' space is free
 
   // ---- merge: warps, then CTAs of the cluster
 #pragma unroll
@@ -583,7 +624,7 @@ __global__ void __launch_bounds__(32 * kKaWarps) kv8_attend_kernel(const __grid_
       ml[warp][0][2 * t + e] = st.m[e];
       ml[warp][1][2 * t + e] = st.l[e];
     }
-    float* dst = &part[warp][t * kKaHeadPair + e * kDim + 16 * g];
+    float* dst = part + warp * kKaPart + t * kKaHeadPair + e * kDim + 16 * g;
     float4* d4 = reinterpret_cast<float4*>(dst);
     d4[0] = make_float4(st.acc[0][e], st.acc[1][e], st.acc[2][e], st.acc[3][e]);
     d4[1] = make_float4(st.acc[4][e], st.acc[5][e], st.acc[6][e], st.acc[7][e]);
@@ -591,27 +632,24 @@ __global__ void __launch_bounds__(32 * kKaWarps) kv8_attend_kernel(const __grid_
     d4[3] = make_float4(st.acc[4][e + 2], st.acc[5][e + 2], st.acc[6][e + 2], st.acc[7][e + 2]);
   }
   bad = __syncthreads_or(bad) != 0;
-  {
-    for (int hd = 0; hd < G; ++hd) {  // thread = dimension
-      float top = ml[0][0][hd];
-#pragma unroll
-      for (int w = 1; w < kKaWarps; ++w) top = fmaxf(top, ml[w][0][hd]);
-      float o = 0.f, l = 0.f;
-      const int at = (hd >> 1) * kKaHeadPair + (hd & 1) * kDim + tid;
-#pragma unroll
-      for (int w = 0; w < kKaWarps; ++w) {
-        const float f = weight(ml[w][0][hd], top);
-        o = fmaf(f, part[w][at], o);
-        l = fmaf(f, ml[w][1][hd], l);
-      }
-      part[0][at] = o;  // read and written by this thread alone
-      if (tid == 0) {
-        cta_ml[0][hd] = top;
-        cta_ml[1][hd] = l;
-      }
+  for (int i = tid; i < G * kDim; i += threads) {
+    const int hd = i / kDim, d = i % kDim;
+    float top = ml[0][0][hd];
+    for (int w = 1; w < n_warps; ++w) top = fmaxf(top, ml[w][0][hd]);
+    float o = 0.f, l = 0.f;
+    const int at = (hd >> 1) * kKaHeadPair + (hd & 1) * kDim + d;
+    for (int w = 0; w < n_warps; ++w) {
+      const float f = weight(ml[w][0][hd], top);
+      o = fmaf(f, part[w * kKaPart + at], o);
+      l = fmaf(f, ml[w][1][hd], l);
     }
-    if (tid == 0) cta_bad = bad ? 1 : 0;
+    part[at] = o;  // read and written by this thread alone
+    if (d == 0) {
+      cta_ml[0][hd] = top;
+      cta_ml[1][hd] = l;
+    }
   }
+  if (tid == 0) cta_bad = bad ? 1 : 0;
   const auto store = [&](int hd, int d, float v) {
     const size_t at = (static_cast<size_t>(s) * p.hq + static_cast<size_t>(h) * G + hd) * kDim + d;
     if constexpr (F32OUT)
@@ -628,7 +666,7 @@ __global__ void __launch_bounds__(32 * kKaWarps) kv8_attend_kernel(const __grid_
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(dsmem_addr(&cta_bad, r)) : "memory");
     any_bad = any_bad || v != 0;
   }
-  for (int i = tid; i < G * dpc; i += 32 * kKaWarps) {
+  for (int i = tid; i < G * dpc; i += threads) {
     const int hd = i / dpc, d = rank * dpc + i % dpc;
     const int at = (hd >> 1) * kKaHeadPair + (hd & 1) * kDim + d;
     float top = -INFINITY;
@@ -636,7 +674,7 @@ __global__ void __launch_bounds__(32 * kKaWarps) kv8_attend_kernel(const __grid_
     float o = 0.f, l = 0.f;
     for (int r = 0; r < CS; ++r) {
       const float f = weight(ld_dsmem(dsmem_addr(&cta_ml[0][hd], r)), top);
-      o = fmaf(f, ld_dsmem(dsmem_addr(&part[0][at], r)), o);
+      o = fmaf(f, ld_dsmem(dsmem_addr(part + at, r)), o);
       l = fmaf(f, ld_dsmem(dsmem_addr(&cta_ml[1][hd], r)), l);
     }
     store(hd, d, any_bad ? 0.f : o / l);
@@ -649,11 +687,13 @@ __global__ void __launch_bounds__(32 * kKaWarps) kv8_attend_kernel(const __grid_
 // ---------------------------------------------------------------- launches
 namespace {
 
-template <typename P>
-cudaError_t launch(void (*k)(P), dim3 grid, int threads, int cluster, cudaStream_t stream, const P& p) {
+template <typename... Args>
+cudaError_t launch(void (*k)(Args...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                   const Args&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute a[2];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -664,7 +704,7 @@ cudaError_t launch(void (*k)(P), dim3 grid, int threads, int cluster, cudaStream
   a[1].val.clusterDim.z = 1;
   cfg.attrs = a;
   cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k, p);
+  return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
 }  // namespace
@@ -673,29 +713,56 @@ cudaError_t launch_kv8_append(int code, const Kv8AppendParams& p, int batch, cud
   // at most (63 + max_new) / 64 blocks are completed
   const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.max_new) + kBlock - 1) / kBlock),
                   static_cast<unsigned>(p.kv.hkv), static_cast<unsigned>(batch));
-  return code == kCodeE4m3 ? launch(kv8_append_kernel<kCodeE4m3>, grid, 256, 0, stream, p)
-                           : launch(kv8_append_kernel<kCodeInt8>, grid, 256, 0, stream, p);
+  return code == kCodeE4m3 ? launch(kv8_append_kernel<kCodeE4m3>, grid, 256, 0, 0, stream, p)
+                           : launch(kv8_append_kernel<kCodeInt8>, grid, 256, 0, 0, stream, p);
 }
 
 cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int batch, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.count) + kBlock - 1) / kBlock),
                   static_cast<unsigned>(p.kv.hkv), static_cast<unsigned>(batch));
   if (code == kCodeE4m3)
-    return f32_out ? launch(kv8_read_kernel<kCodeE4m3, float>, grid, 256, 0, stream, p)
-                   : launch(kv8_read_kernel<kCodeE4m3, __nv_bfloat16>, grid, 256, 0, stream, p);
-  return f32_out ? launch(kv8_read_kernel<kCodeInt8, float>, grid, 256, 0, stream, p)
-                 : launch(kv8_read_kernel<kCodeInt8, __nv_bfloat16>, grid, 256, 0, stream, p);
+    return f32_out ? launch(kv8_read_kernel<kCodeE4m3, float>, grid, 256, 0, 0, stream, p)
+                   : launch(kv8_read_kernel<kCodeE4m3, __nv_bfloat16>, grid, 256, 0, 0, stream, p);
+  return f32_out ? launch(kv8_read_kernel<kCodeInt8, float>, grid, 256, 0, 0, stream, p)
+                 : launch(kv8_read_kernel<kCodeInt8, __nv_bfloat16>, grid, 256, 0, 0, stream, p);
+}
+
+// Two groups a CTA (two such CTAs an SM), and as many CTAs a cluster as keep
+// the whole grid resident at once (2 x 148), up to one block a group.
+// Measured, (CTAs a cluster, groups) -> us: 64 pairs x 32 blocks (8, 1) 14.0,
+// (8, 2) 20.8, (4, 2) 11.7, (2, 2) 13.8; 256 pairs x 64 blocks (8, 1) 72.7,
+// (2, 2) 60.2, (1, 2) 53.4; 16 pairs x 2,000 blocks (8, 2) 114, (16, 2) 105.
+Kv8AttendPlan kv8_attend_plan(int pairs, int max_blocks) {
+  Kv8AttendPlan a{};
+  a.groups = 2;
+  a.cluster = 1;
+  while (a.cluster < kKaMaxCluster && pairs * a.cluster * 2 <= 2 * 148 && a.cluster * 2 * a.groups <= max_blocks)
+    a.cluster *= 2;
+  return a;
 }
 
 cudaError_t launch_kv8_attend(int code, bool f32_out, const Kv8AttendParams& p, int batch, cudaStream_t stream) {
-  const int cs = 8;
-  const dim3 grid(static_cast<unsigned>(cs), static_cast<unsigned>(batch * p.kv.hkv));
-  constexpr int T = 32 * kKaWarps;
+  const int pairs = batch * p.kv.hkv;
+  const Kv8AttendPlan a = kv8_attend_plan(pairs, p.sel_idx != nullptr ? p.max_sel : p.kv.blocks);
+  const dim3 grid(static_cast<unsigned>(a.cluster), static_cast<unsigned>(pairs));
+  const int T = 128 * a.groups;
+  const size_t smem = static_cast<size_t>(4 * a.groups) * std::max(kKaStages * kKaSlot, kKaPart * 4);
   if (code == kCodeE4m3)
-    return f32_out ? launch(kv8_attend_kernel<kCodeE4m3, true>, grid, T, cs, stream, p)
-                   : launch(kv8_attend_kernel<kCodeE4m3, false>, grid, T, cs, stream, p);
-  return f32_out ? launch(kv8_attend_kernel<kCodeInt8, true>, grid, T, cs, stream, p)
-                 : launch(kv8_attend_kernel<kCodeInt8, false>, grid, T, cs, stream, p);
+    return f32_out ? launch(kv8_attend_kernel<kCodeE4m3, true>, grid, T, smem, a.cluster, stream, p)
+                   : launch(kv8_attend_kernel<kCodeE4m3, false>, grid, T, smem, a.cluster, stream, p);
+  return f32_out ? launch(kv8_attend_kernel<kCodeInt8, true>, grid, T, smem, a.cluster, stream, p)
+                 : launch(kv8_attend_kernel<kCodeInt8, false>, grid, T, smem, a.cluster, stream, p);
+}
+
+cudaError_t prepare_kv8_kernels() {
+  constexpr int smem = kKaMaxWarps * std::max(kKaStages * kKaSlot, kKaPart * 4);
+  for (auto* k : {kv8_attend_kernel<kCodeE4m3, false>, kv8_attend_kernel<kCodeE4m3, true>,
+                  kv8_attend_kernel<kCodeInt8, false>, kv8_attend_kernel<kCodeInt8, true>}) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace sas
