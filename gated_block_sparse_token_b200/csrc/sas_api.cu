@@ -1111,6 +1111,9 @@ sas_status sas_pool_keys_kv8(const sas_config* cfg, const sas_kv8* kv, const int
   p.gk16 = cfg->gate_keys_bf16;
   p.pooled_raw = pooled_raw;
   p.status = static_cast<uint32_t*>(ws);
+  if (num_blocks <= sas::kPoolFewBlocks)
+    return launch_result(
+        sas::launch_pool_few_kv8(kv->code, p, kv->batch, reinterpret_cast<cudaStream_t>(stream)));
   CUtensorMap tmwk;
   if (!encode_kv_map(&tmwk, w_k, static_cast<long long>(cfg->num_kv_heads) * sas::kPool)) return SAS_ERR_CUDA;
   return launch_result(

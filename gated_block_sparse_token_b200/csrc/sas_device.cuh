@@ -511,6 +511,12 @@ __device__ __forceinline__ float f16_hi(uint32_t x) {
   asm("{.reg .b16 a, b; mov.b32 {a, b}, %1; cvt.f32.f16 %0, b;}" : "=f"(r) : "r"(x));
   return r;
 }
+// s + the low / high f16 of x, in fp32 (one instruction each on sm_100).
+__device__ __forceinline__ void add_f16x2(float& s0, float& s1, uint32_t x) {
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; add.rn.f32.f16 %0, a, %0; add.rn.f32.f16 %1, b, %1;}"
+      : "+f"(s0), "+f"(s1)
+      : "r"(x));
+}
 __device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -390,16 +390,17 @@ struct NormRopeGrid {
   int x, chunk, q_chunks, k_chunks;
 };
 
-// Heads of a CTA: as many as leave about two waves of full SMs (148 SMs x 8
-// CTAs of 256 threads), so that the angles are shared by many heads of a long
-// batch while a decode step's few rows spread over the SMs.  The gradient
-// keeps at most kNrMaxCtas CTAs, which then walk the tokens.
+// Heads of a CTA: as many as leave two waves of resident CTAs (148 SMs x 4; the
+// gradient one wave of 148 x 2), so that the angles are shared by many heads of
+// a long batch while a decode step's few rows spread over the SMs.  A forward
+// CTA takes at most 16 (32,768 tokens: 8 heads 243 us, 16 heads 238, all 32
+// 254).  The gradient keeps at most kNrMaxCtas CTAs, which then walk the tokens.
 inline NormRopeGrid norm_rope_grid(int batch, int tokens, int hq, int hkv, bool back) {
   const long long slots = (static_cast<long long>(batch) * tokens + kNrThreads / 8 - 1) / (kNrThreads / 8);
   const int most = std::max(std::max(hq, hkv), 1);
-  const long long want = slots * (hq + hkv) / (148 * 16);
+  const long long want = slots * (hq + hkv) / (back ? 148 * 2 : 148 * 8);
   NormRopeGrid g{};
-  g.chunk = static_cast<int>(std::min<long long>(std::max<long long>(want, 1), std::min(most, 8)));
+  g.chunk = static_cast<int>(std::min<long long>(std::max<long long>(want, 1), back ? most : std::min(most, 16)));
   for (;; ++g.chunk) {
     g.q_chunks = (hq + g.chunk - 1) / g.chunk;
     g.k_chunks = (hkv + g.chunk - 1) / g.chunk;
@@ -485,6 +486,9 @@ cudaError_t launch_kv8_attend(int code, bool f32_out, const Kv8AttendParams& p, 
 // pooling over the 8-bit cache: p.kv.k holds the codes, p.k_scale the scales
 cudaError_t launch_pool_project_kv8(int code, const PoolParams& p, const CUtensorMap& tmwk, int batch,
                                     cudaStream_t stream);
+// the same with one CTA a block, for up to kPoolFewBlocks blocks a sequence
+constexpr int kPoolFewBlocks = 4;
+cudaError_t launch_pool_few_kv8(int code, const PoolParams& p, int batch, cudaStream_t stream);
 
 // One-time per-process set-up of kernel attributes.
 cudaError_t prepare_kernels();

@@ -46,7 +46,7 @@ __device__ __forceinline__ uint4 load_new_row(const RowsView& r, long long tok, 
 }
 
 template <int CODE>
-__global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
+__global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int s = blockIdx.z, h = blockIdx.y;
@@ -59,21 +59,13 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
              static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
   if (!err && n == 0) return;  // uniform over the CTA, like every branch on n and L
   const int b_first = err ? 0 : L0 / kBlock, b_done = err ? 0 : L / kBlock;  // completed: [b_first, b_done)
-  // a page out of range anywhere in the write skips the whole (sequence, head)
-  for (int b = b_first + static_cast<int>(threadIdx.x); b < b_done && !err; b += 256)
-    if (p.kv.tile(s, h, b) < 0) err = true;
-  __shared__ uint32_t amax_s[2][4];
-  if (__syncthreads_or(err)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(p.status, kStatusBounds);
-    return;
-  }
   const RowsView src = half == 0 ? p.k_new : p.v_new;
   __nv_bfloat16* tail = const_cast<__nv_bfloat16*>(half == 0 ? p.kv.k_tail : p.kv.v_tail) +
                         (static_cast<long long>(s) * p.kv.hkv + h) * (kBlock * kDim);
   const int d0 = 8 * (tid & 15), r0 = tid >> 4;  // 16 lanes a row, rows r0, r0 + 8, ..
   const int b = b_first + static_cast<int>(blockIdx.x);
-  if (b < b_done) {
-    uint4 x[8];
+  uint4 x[8];
+  if (b < b_done) {  // never when err; the rows lie in the input and the tail whatever the pages are
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int row = r0 + 8 * i;
@@ -81,6 +73,17 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
       x[i] = t < 0 ? *reinterpret_cast<const uint4*>(tail + row * kDim + d0)
                    : load_new_row(src, start + t, h, s, d0);
     }
+  }
+  // a page out of range anywhere in the write skips the whole (sequence, head)
+  if (p.kv.block_table != nullptr)
+    for (int k = b_first + static_cast<int>(threadIdx.x); k < b_done; k += 256)
+      if (p.kv.tile(s, h, k) < 0) err = true;
+  __shared__ uint32_t amax_s[2][4];
+  if (__syncthreads_or(err)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(p.status, kStatusBounds);
+    return;
+  }
+  if (b < b_done) {
     uint32_t m = 0;  // two bf16 magnitudes
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -145,9 +148,25 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
 
 // ---------------------------------------------------------------- read-back
 // One CTA per (64 output tokens, KV head, sequence), threads 0-127 the keys,
-// 128-255 the values; 8 lanes a row, 16 codes a lane.
+// 128-255 the values; 8 lanes a row, 16 codes a lane, four rows a thread whose
+// loads go out together.  The 64 tokens lie in two blocks at most.
+template <typename OutT>
+__device__ __forceinline__ void store16(OutT* dst, const float (&x)[16]) {
+  if constexpr (std::is_same_v<OutT, float>) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      reinterpret_cast<float4*>(dst)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      reinterpret_cast<uint4*>(dst)[k] =
+          make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
+                     pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
+  }
+}
+
 template <int CODE, typename OutT>
-__global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
+__global__ void __launch_bounds__(256, 5) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int s = blockIdx.z, h = blockIdx.y;
@@ -156,63 +175,78 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ K
   const int begin = p.begin != nullptr ? p.begin[s] : 0;
   const RowsView o = half == 0 ? p.k_out : p.v_out;
   bool err = L < 1 || begin < 0 || static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
-  if (o.data != nullptr && !err) {
-    const int c = (L - 1) / kBlock;
-    const int d0 = 16 * (tid & 7);
-    const __nv_bfloat16* tail = (half == 0 ? p.kv.k_tail : p.kv.v_tail) +
-                                (static_cast<long long>(s) * p.kv.hkv + h) * (kBlock * kDim);
+  // tokens of this CTA: positions first .. first + n - 1
+  const int t0 = static_cast<int>(blockIdx.x) * kBlock;
+  const long long first = static_cast<long long>(begin) + t0;
+  const int n = err ? 0 : static_cast<int>(min(static_cast<long long>(min(kBlock, p.count - t0)), L - first));
+  if (o.data != nullptr && n > 0) {
+    const int c = (L - 1) / kBlock, b0 = static_cast<int>(first / kBlock), off = static_cast<int>(first % kBlock);
     const uint8_t* codes = half == 0 ? p.kv.k : p.kv.v;
     const float* scales = half == 0 ? p.kv.k_scale : p.kv.v_scale;
+    // the two blocks: tile and scale (scale 0 and tile -1: a page out of range)
+    long long tile0 = -1, tile1 = -1;
+    float sc0 = 0.f, sc1 = 0.f;
+    if (b0 < c) {
+      tile0 = p.kv.tile(s, h, b0);
+      if (tile0 >= 0) sc0 = scales[tile0];
+      if (tile0 < 0) err = true;
+    }
+    if (b0 + 1 < c && off + n > kBlock) {
+      tile1 = p.kv.tile(s, h, b0 + 1);
+      if (tile1 >= 0) sc1 = scales[tile1];
+      if (tile1 < 0) err = true;
+    }
+    const int d0 = 16 * (tid & 7), r0 = tid >> 3;  // rows r0, r0 + 16, ..
     OutT* out = static_cast<OutT*>(const_cast<void*>(o.data)) + static_cast<long long>(s) * o.seq +
-                static_cast<long long>(h) * o.head + d0;
+                static_cast<long long>(h) * o.head + static_cast<long long>(t0) * o.token + d0;
+    uint4 w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = static_cast<int>(blockIdx.x) * kBlock + (tid >> 3) + 16 * i;
-      const long long pos = static_cast<long long>(begin) + t;
-      if (t >= p.count || pos >= L) continue;
-      const int b = static_cast<int>(pos / kBlock), row = static_cast<int>(pos % kBlock);
+      const int t = r0 + 16 * i, at = off + t;
+      const long long tile = at < kBlock ? tile0 : tile1;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (t < n && tile >= 0)
+        w[i] = *reinterpret_cast<const uint4*>(codes + tile * kTile8Bytes + (at & (kBlock - 1)) * kDim + d0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = r0 + 16 * i, at = off + t;
+      if (t >= n || b0 + (at >= kBlock) >= c) continue;  // past the end, or the current block (below)
+      const float sc = at < kBlock ? sc0 : sc1;
+      const bool known = (at < kBlock ? tile0 : tile1) >= 0;
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
       float x[16];
-      if (b == c) {
-        const uint4* w = reinterpret_cast<const uint4*>(tail + row * kDim + d0);
-        const uint4 w0 = w[0], w1 = w[1];
-        const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t lo, hi;
+        codes_f16<CODE>(u[k], lo, hi);
+        x[4 * k] = f16_lo(lo) * sc;
+        x[4 * k + 1] = f16_hi(lo) * sc;
+        x[4 * k + 2] = f16_lo(hi) * sc;
+        x[4 * k + 3] = f16_hi(hi) * sc;
+      }
+      if (!known) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = 0.f;
+      }
+      store16(out + static_cast<long long>(t) * o.token, x);
+    }
+    if (b0 + 1 >= c) {  // rows of the current block: from the tail
+      const __nv_bfloat16* tail = (half == 0 ? p.kv.k_tail : p.kv.v_tail) +
+                                  (static_cast<long long>(s) * p.kv.hkv + h) * (kBlock * kDim);
+      for (int t = r0; t < n; t += 16) {
+        const int at = off + t;
+        if (b0 + (at >= kBlock) != c) continue;
+        const uint4* v = reinterpret_cast<const uint4*>(tail + (at & (kBlock - 1)) * kDim + d0);
+        const uint4 v0 = v[0], v1 = v[1];
+        const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        float x[16];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           x[2 * k] = bf16_lo(u[k]);
           x[2 * k + 1] = bf16_hi(u[k]);
         }
-      } else {
-        const long long tile = p.kv.tile(s, h, b);
-        if (tile < 0) {
-          err = true;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = 0.f;
-        } else {
-          const float sc = scales[tile];
-          const uint4 w = *reinterpret_cast<const uint4*>(codes + tile * kTile8Bytes + row * kDim + d0);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t lo, hi;
-            codes_f16<CODE>(u[k], lo, hi);
-            x[4 * k] = f16_lo(lo) * sc;
-            x[4 * k + 1] = f16_hi(lo) * sc;
-            x[4 * k + 2] = f16_lo(hi) * sc;
-            x[4 * k + 3] = f16_hi(hi) * sc;
-          }
-        }
-      }
-      OutT* dst = out + static_cast<long long>(t) * o.token;
-      if constexpr (std::is_same_v<OutT, float>) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          reinterpret_cast<float4*>(dst)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          reinterpret_cast<uint4*>(dst)[k] =
-              make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
-                         pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
+        store16(out + static_cast<long long>(t) * o.token, x);
       }
     }
   }

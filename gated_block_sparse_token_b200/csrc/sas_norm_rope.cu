@@ -24,15 +24,25 @@ namespace {
 
 constexpr int kNrRowsPerCta = kNrThreads / 8;  // token slots of a CTA
 
-// 8 consecutive elements as fp32 (16-byte aligned).
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
+// 8 consecutive elements as loaded (16-byte aligned), and as fp32.
+template <typename T>
+struct Raw8 {
+  uint4 r[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, Raw8<T>& x) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) x.r[i] = reinterpret_cast<const uint4*>(p)[i];
+}
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& v, float (&x)[8]) {
+  const uint4 r = v.r[0];
   x[0] = bf16_lo(r.x), x[1] = bf16_hi(r.x), x[2] = bf16_lo(r.y), x[3] = bf16_hi(r.y);
   x[4] = bf16_lo(r.z), x[5] = bf16_hi(r.z), x[6] = bf16_lo(r.w), x[7] = bf16_hi(r.w);
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+__device__ __forceinline__ void unpack8(const Raw8<float>& v, float (&x)[8]) {
+  const uint4 a = v.r[0], b = v.r[1];
+  x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
+  x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y), x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
@@ -55,7 +65,7 @@ __device__ __forceinline__ float sum8lanes(float v) {
 // blockIdx.y: a chunk of p.chunk heads, the query heads' chunks first (a
 // chunk never mixes queries and keys); blockIdx.x: tokens, 32 at a time.
 template <typename T, bool kBack>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, j = lane & 7;
@@ -81,29 +91,40 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_cons
     const int s = n / p.tokens, t = n - s * p.tokens;
     const int pos = n < n_tok ? (p.positions != nullptr ? p.positions[n] : t) : -1;
     const bool live = pos >= 0;  // uniform over the 8 lanes of a row
-    float cs[8], sn[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) rope_cos_sin(p.rope.theta_over_pi[8 * j + e], max(pos, 0), cs[e], sn[e]);
     const long long off = static_cast<long long>(s) * xv.seq + static_cast<long long>(t) * xv.token + 8 * j;
     const T* x = static_cast<const T*>(xv.data) + off;
     T* y = static_cast<T*>(const_cast<void*>(yv.data)) + static_cast<long long>(s) * yv.seq +
            static_cast<long long>(t) * yv.token + 8 * j;
     const T* dy = static_cast<const T*>(dv.data) + static_cast<long long>(s) * dv.seq +
                   static_cast<long long>(t) * dv.token + 8 * j;
-#pragma unroll 2
+    // the next head's loads go out before this one's store, which the compiler
+    // could not arrange: the output may be the input.  (Two and four heads ahead
+    // cost the forward its fourth CTA an SM: 254 and 283 us against 238 for
+    // 2 x 32,768 tokens of 32 + 8 heads.)
+    Raw8<T> bx[2], bd[2];
+    auto fetch = [&](int h) {
+      load8(x + h * xv.head, bx[0]);
+      load8(x + h * xv.head + 64, bx[1]);
+      if constexpr (kBack) {
+        load8(dy + h * dv.head, bd[0]);
+        load8(dy + h * dv.head + 64, bd[1]);
+      }
+    };
+    bx[0] = bx[1] = bd[0] = bd[1] = Raw8<T>{};
+    if (live) fetch(h0);
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rope_cos_sin(p.rope.theta_over_pi[8 * j + e], max(pos, 0), cs[e], sn[e]);
     for (int h = h0; h < h1; ++h) {
       float lo[8], hi[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) lo[e] = hi[e] = 0.f;
-      if (live) {
-        load8(x + h * xv.head, lo);
-        load8(x + h * xv.head + 64, hi);
-      }
+      unpack8(bx[0], lo);
+      unpack8(bx[1], hi);
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], ss));
-      const float r = rsqrtf(sum8lanes(ss) * (1.f / kDim) + p.eps);
       if constexpr (!kBack) {
+        if (live && h + 1 < h1) fetch(h + 1);
+        const float r = rsqrtf(sum8lanes(ss) * (1.f / kDim) + p.eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float a = lo[e] * r * glo[e], b = hi[e] * r * ghi[e];
@@ -112,12 +133,10 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_cons
         }
       } else {
         float dlo[8], dhi[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dlo[e] = dhi[e] = 0.f;
-        if (live) {
-          load8(dy + h * dv.head, dlo);
-          load8(dy + h * dv.head + 64, dhi);
-        }
+        unpack8(bd[0], dlo);
+        unpack8(bd[1], dhi);
+        if (live && h + 1 < h1) fetch(h + 1);
+        const float r = rsqrtf(sum8lanes(ss) * (1.f / kDim) + p.eps);
         float dot = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {

@@ -258,48 +258,58 @@ constexpr int kPpSmem = kPpA + kPpB + 2 * kPpRows * 4 + 64 + 1024;
 
 enum PoolSource : int { kSrcE4m3 = kCodeE4m3, kSrcInt8 = kCodeInt8, kSrcBf16 };
 
-// Pooled codes of one 64-token tile: maximum, minimum (f16x2, exact) and sum
-// (fp32, exact: multiples of 2^-9 below 2^15) of dims 16 cvec .. 16 cvec + 15,
-// cvec = lane % 8, over all 64 rows, in every lane.
-template <int CODE>
-__device__ __forceinline__ void pool_codes(const uint8_t* tile, int lane, uint32_t (&mx)[8], uint32_t (&mn)[8],
-                                           float (&sm)[16]) {
-  const uint8_t* src = tile + (lane >> 3) * kDim + 16 * (lane & 7);
-  uint4 raw[16];
+// Pooled codes of dims 4 lane .. 4 lane + 3 over ROWS rows of a tile, the first
+// at src (the lane's four codes of it): maximum and minimum as f16 pairs (dims
+// 0, 1 and 2, 3), the sums in fp32 -- all exact (sums are multiples of 2^-9
+// below 2^15).  A lane reads its 4 bytes of every row, so nothing is left to
+// reduce across lanes.  int8 codes stay biased by 1152 until the end (exact
+// in f16): taking the bias off each would cost as much as the maxima.
+template <int CODE, int ROWS>
+__device__ __forceinline__ void pool_codes(const uint8_t* src, float (&mx)[4], float (&mn)[4], float (&sm)[4]) {
+  constexpr int STEP = ROWS < 32 ? ROWS : 32;  // rows in flight
+  uint32_t hx[2] = {0u, 0u}, hn[2] = {0u, 0u};
 #pragma unroll
-  for (int r = 0; r < 16; ++r) raw[r] = *reinterpret_cast<const uint4*>(src + 4 * r * kDim);
+  for (int v = 0; v < 4; ++v) sm[v] = 0.f;
 #pragma unroll
-  for (int v = 0; v < 16; ++v) sm[v] = 0.f;
+  for (int r0 = 0; r0 < ROWS; r0 += STEP) {
+    uint32_t raw[STEP];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
+    for (int r = 0; r < STEP; ++r) raw[r] = *reinterpret_cast<const uint32_t*>(src + (r0 + r) * kDim);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
+    for (int r = 0; r < STEP; ++r) {
       uint32_t c[2];
-      codes_f16<CODE>(w[v], c[0], c[1]);
+      if constexpr (CODE == kCodeE4m3) {
+        codes_f16<CODE>(raw[r], c[0], c[1]);
+      } else {
+        const uint32_t w = raw[r] ^ 0x80808080u;
+        c[0] = __byte_perm(w, 0x64646464u, 0x4140);
+        c[1] = __byte_perm(w, 0x64646464u, 0x4342);
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        mx[2 * v + k] = r == 0 ? c[k] : max_f16x2(mx[2 * v + k], c[k]);
-        mn[2 * v + k] = r == 0 ? c[k] : min_f16x2(mn[2 * v + k], c[k]);
-        sm[4 * v + 2 * k] += f16_lo(c[k]);
-        sm[4 * v + 2 * k + 1] += f16_hi(c[k]);
+        hx[k] = r0 + r == 0 ? c[k] : max_f16x2(hx[k], c[k]);
+        hn[k] = r0 + r == 0 ? c[k] : min_f16x2(hn[k], c[k]);
+        add_f16x2(sm[2 * k], sm[2 * k + 1], c[k]);
       }
     }
   }
+  constexpr float bias = CODE == kCodeInt8 ? 1152.f : 0.f;
 #pragma unroll
-  for (int o = 8; o < 32; o <<= 1) {
-#pragma unroll
-    for (int v = 0; v < 8; ++v) {
-      mx[v] = max_f16x2(mx[v], __shfl_xor_sync(0xffffffffu, mx[v], o));
-      mn[v] = min_f16x2(mn[v], __shfl_xor_sync(0xffffffffu, mn[v], o));
-    }
-#pragma unroll
-    for (int v = 0; v < 16; ++v) sm[v] += __shfl_xor_sync(0xffffffffu, sm[v], o);
+  for (int k = 0; k < 2; ++k) {
+    mx[2 * k] = f16_lo(hx[k]) - bias, mx[2 * k + 1] = f16_hi(hx[k]) - bias;
+    mn[2 * k] = f16_lo(hn[k]) - bias, mn[2 * k + 1] = f16_hi(hn[k]) - bias;
   }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) sm[v] -= ROWS * bias;
 }
 
+// Threads of the kernel for a source: codes are pooled by sixteen warps (the
+// loop over a block's words is bound by instruction issue, half the bytes a
+// word more than for bf16), of which the first eight run the epilogue.
+__host__ __device__ constexpr int pp_threads(int src) { return src == kSrcBf16 ? kPpThreads : 2 * kPpThreads; }
+
 template <int SRC>
-__global__ void __launch_bounds__(kPpThreads, 1) pool_project_kernel(const __grid_constant__ PoolParams p,
+__global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const __grid_constant__ PoolParams p,
                                                                      const __grid_constant__ CUtensorMap tmwk) {
   const int s = blockIdx.z;
   const int h = blockIdx.y;
@@ -347,52 +357,35 @@ __global__ void __launch_bounds__(kPpThreads, 1) pool_project_kernel(const __gri
   // ---- pooling into the A operand
   if constexpr (SRC != kSrcBf16) {
     bool err = false;
-    for (int i = warp; i < kPpRows; i += kPpThreads / 32) {  // warp-uniform
+    for (int i = warp; i < kPpRows; i += pp_threads(SRC) / 32) {  // warp-uniform
       const long long row = row_of(i);
       if (row == -2) err = true;
-      uint32_t mx[8], mn[8];
-      float sm[16];
-      if (row >= 0) {
-        pool_codes<SRC>(static_cast<const uint8_t*>(p.kv.k) + row * kDim, lane, mx, mn, sm);
-      } else {
+      float mx[4] = {0.f, 0.f, 0.f, 0.f}, mn[4] = {0.f, 0.f, 0.f, 0.f}, sm[4] = {0.f, 0.f, 0.f, 0.f};
+      if (row >= 0) pool_codes<SRC, kBlock>(static_cast<const uint8_t*>(p.kv.k) + row * kDim + 4 * lane, mx, mn, sm);
+      uint32_t pk[4][2];
 #pragma unroll
-        for (int v = 0; v < 8; ++v) mx[v] = mn[v] = 0u;
-#pragma unroll
-        for (int v = 0; v < 16; ++v) sm[v] = 0.f;
+      for (int v = 0; v < 2; ++v) {
+        const float m0 = sm[2 * v] * (1.f / kBlock), m1 = sm[2 * v + 1] * (1.f / kBlock);
+        const float g0 = __bfloat162float(__float2bfloat16_rn(m0)), g1 = __bfloat162float(__float2bfloat16_rn(m1));
+        pk[0][v] = pack_bf16x2(mx[2 * v], mx[2 * v + 1]);
+        pk[1][v] = pack_bf16x2(mn[2 * v], mn[2 * v + 1]);
+        pk[2][v] = pack_bf16x2(g0, g1);
+        pk[3][v] = pack_bf16x2(m0 - g0, m1 - g1);
       }
-      if (lane < 8) {
-        const int cvec = lane;  // dims 16 cvec ..: chunk 2 sec + cvec / 4, 16-byte units 2 (cvec % 4) and the next
-        uint32_t pk[4][8];
+      // K index sec * 128 + 4 lane: chunk 2 sec + lane / 16, 16-byte unit (lane / 2) % 8, half lane % 2
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          const float m0 = sm[2 * v] * (1.f / kBlock), m1 = sm[2 * v + 1] * (1.f / kBlock);
-          const float g0 = __bfloat162float(__float2bfloat16_rn(m0)), g1 = __bfloat162float(__float2bfloat16_rn(m1));
-          pk[0][v] = pack_bf16x2(f16_lo(mx[v]), f16_hi(mx[v]));
-          pk[1][v] = pack_bf16x2(f16_lo(mn[v]), f16_hi(mn[v]));
-          pk[2][v] = pack_bf16x2(g0, g1);
-          pk[3][v] = pack_bf16x2(m0 - g0, m1 - g1);
-        }
+      for (int sec = 0; sec < 4; ++sec)
+        *reinterpret_cast<uint2*>(sA + (2 * sec + (lane >> 4)) * (kPpRows * 128) + i * 128 +
+                                  ((((lane >> 1) & 7) ^ (i & 7)) << 4) + 8 * (lane & 1)) =
+            make_uint2(pk[sec][0], pk[sec][1]);
+      if (p.pooled_raw != nullptr && row >= 0) {
+        const float sc = p.k_scale[row / kBlock];
+        float* pr = p.pooled_raw + ((static_cast<size_t>(s) * p.hkv + h) * p.mg + (b0 + i)) * kPool + lane * 4;
 #pragma unroll
-        for (int sec = 0; sec < 4; ++sec) {
-          uint8_t* dst = sA + (2 * sec + (cvec >> 2)) * (kPpRows * 128) + i * 128;
-          const int j = 2 * (cvec & 3);
-          *reinterpret_cast<uint4*>(dst + ((j ^ (i & 7)) << 4)) =
-              make_uint4(pk[sec][0], pk[sec][1], pk[sec][2], pk[sec][3]);
-          *reinterpret_cast<uint4*>(dst + (((j + 1) ^ (i & 7)) << 4)) =
-              make_uint4(pk[sec][4], pk[sec][5], pk[sec][6], pk[sec][7]);
-        }
-        if (p.pooled_raw != nullptr && row >= 0) {
-          const float sc = p.k_scale[row / kBlock];
-          float* pr = p.pooled_raw + ((static_cast<size_t>(s) * p.hkv + h) * p.mg + (b0 + i)) * kPool + cvec * 16;
-#pragma unroll
-          for (int v = 0; v < 8; ++v) {  // 4-byte aligned: scalar stores
-            pr[2 * v] = f16_lo(mx[v]) * sc;
-            pr[2 * v + 1] = f16_hi(mx[v]) * sc;
-            pr[kDim + 2 * v] = f16_lo(mn[v]) * sc;
-            pr[kDim + 2 * v + 1] = f16_hi(mn[v]) * sc;
-            pr[2 * kDim + 2 * v] = sm[2 * v] * (1.f / kBlock) * sc;
-            pr[2 * kDim + 2 * v + 1] = sm[2 * v + 1] * (1.f / kBlock) * sc;
-          }
+        for (int v = 0; v < 4; ++v) {  // 4-byte aligned: scalar stores
+          pr[v] = mx[v] * sc;
+          pr[kDim + v] = mn[v] * sc;
+          pr[2 * kDim + v] = sm[v] * (1.f / kBlock) * sc;
         }
       }
     }
@@ -509,11 +502,14 @@ __global__ void __launch_bounds__(kPpThreads, 1) pool_project_kernel(const __gri
     const int q4 = warp & 3, hf = warp >> 2;  // lane quarter; half of the rotate-half pairs
     const int i = 32 * q4 + lane;             // tile row = block b0 + i
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+    const bool mine = SRC == kSrcBf16 || hf < 2;  // warp-uniform
     float lo[32], hi[32];
-    tmem_ld32(tl + 32 * hf, lo);       // columns 32 hf .. 32 hf + 31
-    tmem_ld32(tl + 64 + 32 * hf, hi);  // their rotate-half partners
-    tmem_wait_ld();
-    const long long row = row_of(i);
+    if (mine) {
+      tmem_ld32(tl + 32 * hf, lo);       // columns 32 hf .. 32 hf + 31
+      tmem_ld32(tl + 64 + 32 * hf, hi);  // their rotate-half partners
+      tmem_wait_ld();
+    }
+    const long long row = mine ? row_of(i) : -1;
     if constexpr (SRC != kSrcBf16) {
       const float sc = row >= 0 ? p.k_scale[row / kBlock] : 0.f;
 #pragma unroll
@@ -522,10 +518,12 @@ __global__ void __launch_bounds__(kPpThreads, 1) pool_project_kernel(const __gri
         hi[k] *= sc;
       }
     }
-    float ss = 0.f;
+    if (mine) {
+      float ss = 0.f;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) ss = fmaf(lo[k], lo[k], fmaf(hi[k], hi[k], ss));
-    ssq[hf * kPpRows + i] = ss;
+      for (int k = 0; k < 32; ++k) ss = fmaf(lo[k], lo[k], fmaf(hi[k], hi[k], ss));
+      ssq[hf * kPpRows + i] = ss;
+    }
     __syncthreads();
     if (row >= 0 && okm) {
       const int b = b0 + i;
@@ -580,10 +578,118 @@ cudaError_t launch_pool_project_kv8(int code, const PoolParams& p, const CUtenso
   const dim3 grid(static_cast<unsigned>((p.num_blocks + kPpRows - 1) / kPpRows), static_cast<unsigned>(p.hkv),
                   static_cast<unsigned>(batch));
   if (code == kCodeE4m3)
-    pool_project_kernel<kSrcE4m3><<<grid, kPpThreads, kPpSmem, stream>>>(p, tmwk);
+    pool_project_kernel<kSrcE4m3><<<grid, pp_threads(kSrcE4m3), kPpSmem, stream>>>(p, tmwk);
   else
-    pool_project_kernel<kSrcInt8><<<grid, kPpThreads, kPpSmem, stream>>>(p, tmwk);
+    pool_project_kernel<kSrcInt8><<<grid, pp_threads(kSrcInt8), kPpSmem, stream>>>(p, tmwk);
   return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- few blocks
+// The gate keys of the few blocks that a decode step or a short append
+// completes: one CTA (16 warps) per block instead of one per 128, so that
+// nothing waits for a 128-row operand.  Warp w holds rows 24w .. 24w + 23 of
+// W_k[h] in registers (requested before the block's codes are known), pools 4 of
+// the block's rows, and multiplies its 24 pooled values once all are in; the
+// sums over warps run in a fixed order, in fp32.
+constexpr int kPfThreads = 512, kPfWarps = kPfThreads / 32, kPfRowsK = kPool / kPfWarps;
+
+template <int CODE>
+__global__ void __launch_bounds__(kPfThreads) pool_few_kernel(const __grid_constant__ PoolParams p) {
+  __shared__ float part[3][kPfWarps][kDim];
+  __shared__ float P[kPool];
+  __shared__ float xs[kDim];
+  __shared__ float ssq[kDim / 32];
+  const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int L = p.kv.seq_lens[s];
+  const int b = (p.blk_begin != nullptr ? p.blk_begin[s] : 0) + static_cast<int>(blockIdx.x);
+  if (b < 0 || b >= p.mg || L < 1 || static_cast<long long>(b + 1) * kBlock > L) return;  // uniform
+  uint2 w[kPfRowsK];
+  const __nv_bfloat16* wk = p.w_k + (static_cast<size_t>(h) * kPool + kPfRowsK * warp) * kDim + 4 * lane;
+#pragma unroll
+  for (int i = 0; i < kPfRowsK; ++i) w[i] = *reinterpret_cast<const uint2*>(wk + i * kDim);
+  const long long row = p.kv.block_row(s, h, b);
+  if (row < 0) {
+    if (tid == 0) raise_status(p.status, kStatusBounds);
+    return;
+  }
+  const float scale = p.k_scale[row / kBlock];
+  {
+    constexpr int R = kBlock / kPfWarps;
+    float mx[4], mn[4], sm[4];
+    pool_codes<CODE, R>(static_cast<const uint8_t*>(p.kv.k) + (row + R * warp) * kDim + 4 * lane, mx, mn, sm);
+    *reinterpret_cast<float4*>(&part[0][warp][4 * lane]) = make_float4(mx[0], mx[1], mx[2], mx[3]);
+    *reinterpret_cast<float4*>(&part[1][warp][4 * lane]) = make_float4(mn[0], mn[1], mn[2], mn[3]);
+    *reinterpret_cast<float4*>(&part[2][warp][4 * lane]) = make_float4(sm[0], sm[1], sm[2], sm[3]);
+  }
+  __syncthreads();
+  const size_t gi = (static_cast<size_t>(s) * p.hkv + h) * p.mg + b;
+  if (tid < kPool) {
+    const int sec = tid / kDim, d = tid % kDim;  // sec is the same in a warp
+    float v = part[sec][0][d];
+#pragma unroll
+    for (int k = 1; k < kPfWarps; ++k) {
+      const float x = part[sec][k][d];
+      v = sec == 0 ? fmaxf(v, x) : (sec == 1 ? fminf(v, x) : v + x);
+    }
+    if (sec == 2) v *= 1.f / kBlock;
+    P[tid] = v;
+    if (p.pooled_raw != nullptr) p.pooled_raw[gi * kPool + tid] = v * scale;
+  }
+  __syncthreads();
+  {
+    float u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kPfRowsK; ++i) {
+      const float x = P[kPfRowsK * warp + i];
+      u[0] = fmaf(x, bf16_lo(w[i].x), u[0]);
+      u[1] = fmaf(x, bf16_hi(w[i].x), u[1]);
+      u[2] = fmaf(x, bf16_lo(w[i].y), u[2]);
+      u[3] = fmaf(x, bf16_hi(w[i].y), u[3]);
+    }
+    *reinterpret_cast<float4*>(&part[0][warp][4 * lane]) = make_float4(u[0], u[1], u[2], u[3]);
+  }
+  __syncthreads();
+  float u = 0.f, gain = 0.f, cs = 0.f, sn = 0.f;
+  if (tid < kDim) {
+    gain = p.gamma_k[tid];
+    rope_cos_sin(p.rope.theta_over_pi[tid & 63], b, cs, sn);
+#pragma unroll
+    for (int k = 0; k < kPfWarps; ++k) u += part[0][k][tid];
+    u *= scale;
+    float sq = u * u;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane == 0) ssq[warp] = sq;
+  }
+  __syncthreads();
+  if (tid < kDim) {
+    u *= 1.f / sqrtf((ssq[0] + ssq[1] + ssq[2] + ssq[3]) / kDim + p.eps) * gain;
+    xs[tid] = u;
+  }
+  __syncthreads();
+  if (tid < kDim) {
+    const float y = tid < 64 ? u * cs - xs[tid + 64] * sn : u * cs + xs[tid - 64] * sn;
+    if (p.gk16)
+      static_cast<__nv_bfloat16*>(p.gate_keys)[gi * kDim + tid] = __float2bfloat16_rn(y);
+    else
+      static_cast<float*>(p.gate_keys)[gi * kDim + tid] = y;
+  }
+}
+
+cudaError_t launch_pool_few_kv8(int code, const PoolParams& p, int batch, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_blocks), static_cast<unsigned>(p.hkv), static_cast<unsigned>(batch));
+  cfg.blockDim = dim3(kPfThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return code == kCodeE4m3 ? cudaLaunchKernelEx(&cfg, pool_few_kernel<kCodeE4m3>, p)
+                           : cudaLaunchKernelEx(&cfg, pool_few_kernel<kCodeInt8>, p);
 }
 
 cudaError_t prepare_pool_project_kernel() {
