@@ -265,15 +265,21 @@ __global__ void __launch_bounds__(256, 5) kv8_read_kernel(const __grid_constant_
 // slice ahead, left too little in flight: 84 us for 32 ragged sequences of
 // 4,096 listed tokens against 59; a ring fed by 2-D TMA from a lane of one of
 // the consuming warps cost that warp the issue of two copies a block.)
-//   S^T = K q^T  m16n8k16 f16: the 16 keys are the rows, the (up to 8) heads
-//                of the group the columns; codes are exact in f16, and the
-//                query is scaled by a power of two per head into f16's range
-//                (its bf16 values stay exact down to 2^-24 of the largest);
+//   S^T = K q^T  the 16 keys are the rows, the (up to 8) heads of the group the
+//                columns.  int8: m16n8k32 on the codes as they are stored, the
+//                query as the signed 8-bit digits of a fixed-point number per
+//                head (two digits, 2^-15 of the head's largest value, for a bf16
+//                output, three, 2^-23, for fp32); its sums are exact.  e4m3:
+//                m16n8k16 f16, the codes converted (exact), the query scaled by
+//                a power of two per head into f16's range (its bf16 values stay
+//                exact down to 2^-24 of the largest).  (The e4m3 form of
+//                m16n8k32 with the query as two e4m3 terms ran slower than the
+//                conversions it saves: 144 us against 114 for 2 x 128k tokens.)
 //   softmax      per head over the columns, fp32, base 2; the running maximum
 //                moves only when it grows by more than 2^8 (any factor common
 //                to p and its sum cancels), so most blocks need one vote and
 //                no shuffles;
-//   O^T += V^T P^T, the P fragment transposed in place by movmatrix.  P is
+//   O^T += V^T P^T  m16n8k16 f16 (codes are exact in f16), the P fragment transposed in place by movmatrix.  P is
 //                rounded to f16 (2^-12 relative, before a bf16 output); for an
 //                fp32 output a second product carries the remainder.  The sum
 //                runs over the unrounded p.
@@ -293,11 +299,65 @@ constexpr int kKaMaxCluster = 16;  // beyond the portable 8: allowed by an attri
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+// D(16x8) += A(16x32) * B(32x8) on signed bytes: lane (g, t) holds bytes
+// 4t .. of row g (a0) and g + 8 (a1), 16 + 4t .. of both (a2, a3), and of
+// column g (b0, b1).
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The query of one head (this lane: 32 of its values as 16 bf16 pairs) as B
+// fragments; set() takes the biased exponent e (1 .. 253) of the head's largest
+// value and returns the unit that the fragments count in.
+template <int CODE, bool F32OUT>
+struct KaQuery {  // int8: sum_n 256^n digit_n; k-step j: b[.][2j], b[.][2j + 1]
+  static constexpr int kDigits = F32OUT ? 3 : 2;
+  uint32_t b[kDigits][8];
+
+  __device__ __forceinline__ float set(const uint32_t (&raw)[16], uint32_t e) {
+    // largest value to below 127/128 of 2^(8 kDigits - 1): every digit is a signed byte
+    constexpr float top = (kDigits == 2 ? 16384.f : 4194304.f) * (127.f / 128.f);
+    const float dn = __uint_as_float((254u - e) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int n = 0; n < kDigits; ++n) b[n][i] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = raw[2 * i + (k >> 1)];
+        int v = __float2int_rn(((k & 1) ? bf16_hi(w) : bf16_lo(w)) * dn * top);
+#pragma unroll
+        for (int n = 0; n < kDigits; ++n) {  // the lowest first
+          const int d = static_cast<int8_t>(v & 0xff);
+          b[n][i] |= static_cast<uint32_t>(d & 0xff) << (8 * k);
+          v = (v - d) >> 8;
+        }
+      }
+    }
+    return __uint_as_float(e << 23) * (1.f / top);
+  }
+};
+template <bool F32OUT>
+struct KaQuery<kCodeE4m3, F32OUT> {  // f16; k-step j: b[2j], b[2j + 1]
+  uint32_t b[16];
+
+  __device__ __forceinline__ float set(const uint32_t (&raw)[16], uint32_t e) {
+    const float dn = __uint_as_float((254u - e) << 23);  // q 2^(127 - e) lies in [0, 4)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i] = pack_f16x2(bf16_lo(raw[i]) * dn, bf16_hi(raw[i]) * dn);
+    return __uint_as_float(e << 23);
+  }
+};
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
@@ -362,29 +422,72 @@ __device__ __forceinline__ void raise_max(KaState& st, const float (&sc)[4]) {
 // g + 8, ...).
 template <int CODE, bool SPLIT>
 __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint32_t vs_addr,
-                                             const uint32_t (&qf)[16], const float (&qs)[2], float ks, float vs) {
+                                             const KaQuery<CODE, SPLIT>& q, const float (&qs)[2], float ks, float vs) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int kr = (2 * (g >> 1) + (g >> 2)) ^ (4 * (g & 1)), vr = 2 * t + (t >> 1);
-  float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
+  uint4 x[4];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const uint32_t at = ks_addr + kr * kDim + (((t + 4 * c) ^ kr) << 4);
-    const uint4 x0 = lds128(at), x1 = lds128(at + 8 * kDim);
-    const uint32_t r0[4] = {x0.x, x0.y, x0.z, x0.w};
-    const uint32_t r1[4] = {x1.x, x1.y, x1.z, x1.w};
+    x[2 * c] = lds128(at);
+    x[2 * c + 1] = lds128(at + 8 * kDim);
+  }
+  const uint32_t at0 = vs_addr + vr * kDim + ((g ^ vr) << 4), at1 = vs_addr + (vr ^ 4) * kDim + ((g ^ vr ^ 4) << 4);
+  const uint4 y0 = lds128(at0), y1 = lds128(at1), y2 = lds128(at0 + 8 * kDim), y3 = lds128(at1 + 8 * kDim);
+  float sc[4];
+  if constexpr (CODE == kCodeInt8) {
+    constexpr int N = KaQuery<CODE, SPLIT>::kDigits;
+    int d[2][N][4] = {};  // independent chains of two products
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t a0, a1, a2, a3;
-      codes_f16<CODE>(r0[j], a0, a2);
-      codes_f16<CODE>(r1[j], a1, a3);
-      mma_f16(c == 0 ? sc : sd, a0, a1, a2, a3, qf[8 * c + 2 * j], qf[8 * c + 2 * j + 1]);
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        mma_s8(d[c][n], x[2 * c].x, x[2 * c + 1].x, x[2 * c].y, x[2 * c + 1].y, q.b[n][4 * c], q.b[n][4 * c + 1]);
+        mma_s8(d[c][n], x[2 * c].z, x[2 * c + 1].z, x[2 * c].w, x[2 * c + 1].w, q.b[n][4 * c + 2], q.b[n][4 * c + 3]);
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sc[e] = fmaf(static_cast<float>(d[0][1][e] + d[1][1][e]), 256.f, static_cast<float>(d[0][0][e] + d[1][0][e]));
+      if constexpr (N == 3) sc[e] = fmaf(static_cast<float>(d[0][N - 1][e] + d[1][N - 1][e]), 65536.f, sc[e]);
     }
+  } else {
+    float d[2][4] = {};  // two chains of products
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t r0[4] = {x[2 * c].x, x[2 * c].y, x[2 * c].z, x[2 * c].w};
+      const uint32_t r1[4] = {x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a0, a1, a2, a3;
+        codes_f16<CODE>(r0[j], a0, a2);
+        codes_f16<CODE>(r1[j], a1, a3);
+        mma_f16(d[c], a0, a1, a2, a3, q.b[8 * c + 2 * j], q.b[8 * c + 2 * j + 1]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[e] = d[0][e] + d[1][e];
+  }
+  // V^T as f16, while those products run: a[j] = dims 16g + j and
+  // 16g + 8 + j of keys 2t, 2t + 1 (0, 1) and 2t + 8, 2t + 9 (2, 3)
+  uint32_t a[8][4];
+  {
+    const uint32_t va[4] = {y0.x, y0.y, y0.z, y0.w}, vb[4] = {y1.x, y1.y, y1.z, y1.w};
+    const uint32_t vc[4] = {y2.x, y2.y, y2.z, y2.w}, vd[4] = {y3.x, y3.y, y3.z, y3.w};
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t sel = hf == 0 ? 0x5140 : 0x7362;
+        const int j = 4 * w + 2 * hf;
+        codes_f16<CODE>(__byte_perm(va[w], vb[w], sel), a[j][0], a[j + 1][0]);
+        codes_f16<CODE>(__byte_perm(va[w + 2], vb[w + 2], sel), a[j][1], a[j + 1][1]);
+        codes_f16<CODE>(__byte_perm(vc[w], vd[w], sel), a[j][2], a[j + 1][2]);
+        codes_f16<CODE>(__byte_perm(vc[w + 2], vd[w + 2], sel), a[j][3], a[j + 1][3]);
+      }
   }
   const float f0 = qs[0] * ks, f1 = qs[1] * ks;
-  sc[0] = (sc[0] + sd[0]) * f0;
-  sc[1] = (sc[1] + sd[1]) * f1;
-  sc[2] = (sc[2] + sd[2]) * f0;
-  sc[3] = (sc[3] + sd[3]) * f1;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sc[e] *= (e & 1) ? f1 : f0;
   raise_max(st, sc);
   float p[4];
 #pragma unroll
@@ -398,34 +501,13 @@ __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint
     e0 = transpose8x8(pack_f16x2(p[0] - f16_lo(h0), p[1] - f16_hi(h0)));
     e1 = transpose8x8(pack_f16x2(p[2] - f16_lo(h1), p[3] - f16_hi(h1)));
   }
-  const uint32_t at0 = vs_addr + vr * kDim + ((g ^ vr) << 4), at1 = vs_addr + (vr ^ 4) * kDim + ((g ^ vr ^ 4) << 4);
-  const uint4 y0 = lds128(at0), y1 = lds128(at1), y2 = lds128(at0 + 8 * kDim), y3 = lds128(at1 + 8 * kDim);
-  const uint32_t va[4] = {y0.x, y0.y, y0.z, y0.w}, vb[4] = {y1.x, y1.y, y1.z, y1.w};
-  const uint32_t vc[4] = {y2.x, y2.y, y2.z, y2.w}, vd[4] = {y3.x, y3.y, y3.z, y3.w};
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {  // dims 4w .. 4w + 3 and 8 + those of the lane's 16
+  for (int j = 0; j < 8; ++j) {
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_f16(o, a[j][0], a[j][1], a[j][2], a[j][3], b0, b1);
+    if constexpr (SPLIT) mma_f16(o, a[j][0], a[j][1], a[j][2], a[j][3], e0, e1);
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const uint32_t sel = hf == 0 ? 0x5140 : 0x7362;
-      uint32_t a0x, a0y, a1x, a1y, a2x, a2y, a3x, a3y;
-      codes_f16<CODE>(__byte_perm(va[w], vb[w], sel), a0x, a0y);
-      codes_f16<CODE>(__byte_perm(va[w + 2], vb[w + 2], sel), a1x, a1y);
-      codes_f16<CODE>(__byte_perm(vc[w], vd[w], sel), a2x, a2y);
-      codes_f16<CODE>(__byte_perm(vc[w + 2], vd[w + 2], sel), a3x, a3y);
-      const int j = 4 * w + 2 * hf;
-      float o[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_f16(o, a0x, a1x, a2x, a3x, b0, b1);
-      mma_f16(u, a0y, a1y, a2y, a3y, b0, b1);
-      if constexpr (SPLIT) {
-        mma_f16(o, a0x, a1x, a2x, a3x, e0, e1);
-        mma_f16(u, a0y, a1y, a2y, a3y, e0, e1);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        st.acc[j][e] = fmaf(o[e], vs, st.acc[j][e]);
-        st.acc[j + 1][e] = fmaf(u[e], vs, st.acc[j + 1][e]);
-      }
-    }
+    for (int e = 0; e < 4; ++e) st.acc[j][e] = fmaf(o[e], vs, st.acc[j][e]);
   }
 }
 
@@ -583,7 +665,7 @@ __global__ void __launch_bounds__(256, 2)
   }
 
   // ---- the query, as B fragments: head g, dims 16t .. and 64 + 16t ..
-  uint32_t qf[16];
+  KaQuery<CODE, F32OUT> qf;
   float qs[2];
   {
     uint32_t mag = 0;
@@ -595,13 +677,10 @@ __global__ void __launch_bounds__(256, 2)
     mag = max(mag & 0xffffu, mag >> 16);
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-    // biased exponent e of the largest value (1 .. 253): q 2^(127-e) lies in [0, 4)
-    const uint32_t e = min(max(mag >> 7, 1u), 253u);
-    const float dn = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) qf[i] = pack_f16x2(bf16_lo(raw[i]) * dn, bf16_hi(raw[i]) * dn);
-    qs[0] = __shfl_sync(0xffffffffu, up, 8 * t) * p.scale_log2;
-    qs[1] = __shfl_sync(0xffffffffu, up, 8 * t + 4) * p.scale_log2;
+    float unit = qf.set(raw, min(max(mag >> 7, 1u), 253u));
+    if (mag >= kBf16Inf) unit = __uint_as_float(0x7fc00000u);  // an infinity or NaN: every logit is NaN
+    qs[0] = __shfl_sync(0xffffffffu, unit, 8 * t) * p.scale_log2;
+    qs[1] = __shfl_sync(0xffffffffu, unit, 8 * t + 4) * p.scale_log2;
   }
 
   KaState st;
