@@ -1120,6 +1120,11 @@ sas_status sas_pool_keys_kv8(const sas_config* cfg, const sas_kv8* kv, const int
       sas::launch_pool_project_kv8(kv->code, p, tmwk, kv->batch, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t sas_sparse_decode_kv8_workspace_bytes(const sas_config* cfg, int32_t batch) {
+  if (check_config(cfg) != SAS_OK || batch <= 0) return ws_header_bytes();
+  return ws_header_bytes() + sas::kv8_attend_scratch_bytes(batch * cfg->num_kv_heads, cfg->num_q_heads / cfg->num_kv_heads);
+}
+
 sas_status sas_sparse_decode_kv8(const sas_config* cfg, const void* q, const sas_kv8* kv, const int32_t* sel_idx,
                                  const int32_t* sel_count, void* out, void* ws, size_t ws_bytes,
                                  sas_stream_t stream) {
@@ -1143,7 +1148,11 @@ sas_status sas_sparse_decode_kv8(const sas_config* cfg, const void* q, const sas
   p.out = out;
   p.status = static_cast<uint32_t*>(ws);
   if (prepare() != cudaSuccess) return SAS_ERR_CUDA;
-  return launch_result(sas::launch_kv8_attend(kv->code, cfg->out_dtype == SAS_DTYPE_F32, p, kv->batch,
+  p.batch = kv->batch;
+  p.ws_part = ws_bytes >= sas_sparse_decode_kv8_workspace_bytes(cfg, kv->batch)
+                  ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ws_header_bytes())
+                  : nullptr;
+  return launch_result(sas::launch_kv8_attend(kv->code, cfg->out_dtype == SAS_DTYPE_F32, p,
                                               reinterpret_cast<cudaStream_t>(stream)));
 }
 

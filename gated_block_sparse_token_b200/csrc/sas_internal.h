@@ -465,12 +465,15 @@ struct Kv8ReadParams {
 
 struct Kv8AttendParams {
   Kv8View kv;
+  int batch;
+  int target;                  // chunks: the number of equal ones that sizes them
   int hq, G, max_sel;
   float scale_log2;            // attn_scale * log2(e)
   const __nv_bfloat16* q;      // [B][Hq][128]
   const int32_t* sel_idx;      // [B][Hkv][max_sel], or null: every block
   const int32_t* sel_count;
   void* out;                   // [B][Hq][128]
+  float* ws_part;              // chunks' partial sums, or null: not given
   uint32_t* status;
 };
 
@@ -482,7 +485,8 @@ struct Kv8AttendPlan {
   int cluster, groups;
 };
 Kv8AttendPlan kv8_attend_plan(int pairs, int max_blocks);
-cudaError_t launch_kv8_attend(int code, bool f32_out, const Kv8AttendParams& p, int batch, cudaStream_t stream);
+size_t kv8_attend_scratch_bytes(int pairs, int G);
+cudaError_t launch_kv8_attend(int code, bool f32_out, Kv8AttendParams p, cudaStream_t stream);
 // pooling over the 8-bit cache: p.kv.k holds the codes, p.k_scale the scales
 cudaError_t launch_pool_project_kv8(int code, const PoolParams& p, const CUtensorMap& tmwk, int batch,
                                     cudaStream_t stream);

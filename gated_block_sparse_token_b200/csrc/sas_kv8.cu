@@ -290,12 +290,22 @@ __global__ void __launch_bounds__(256, 5) kv8_read_kernel(const __grid_constant_
 // conflicts.  The block's two scales enter as fp32 factors of S and O.
 // The current block comes from the bf16 tail on bf16 products (P as a sum of
 // two bf16 terms), rows past the length masked, while the ring first fills.
+//
+// Two ways to divide the work.  Lists (and dense attention without the
+// workspace for the other way): a cluster of CTAs a pair, which merge through
+// distributed shared memory.  Dense attention (CHUNKS): every sequence in chunks
+// of equal length, one CTA a (chunk, head), so that few or ragged long
+// sequences fill the SMs; a second kernel merges the chunks' partial sums
+// (16 pairs x 2,000 blocks: clusters of 8 114-121 us, of 16, which not every
+// GPC holds twice, 105-118).
 constexpr int kKaStages = 3;                       // ring slots of a warp
 constexpr int kKaSlot = 2 * 16 * kDim;             // 16 rows of K, then of V
 constexpr int kKaHeadPair = 2 * kDim + 4;  // floats between head pairs of a partial (bank spread)
 constexpr int kKaPart = (kMaxGroup / 2) * kKaHeadPair;
 constexpr int kKaMaxWarps = 8;
-constexpr int kKaMaxCluster = 16;  // beyond the portable 8: allowed by an attribute
+constexpr int kKaMaxChunkBatch = 1024;  // sequences that the chunked way handles
+constexpr int kKaChunkMin = 16;         // blocks of a chunk, at least
+constexpr int kKaMaxCluster = 8;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -567,7 +577,84 @@ __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt
 
 }  // namespace
 
-template <int CODE, bool F32OUT>
+// How dense attention is cut: sequence s of m_s blocks into ceil(m_s / size)
+// chunks; chunk q of head h of it is the grid's number
+// (first_s * Hkv + h * chunks_s + q), first_s the chunks of the sequences before.
+struct KaChunk {
+  int s, h, q, chunks, size;
+};
+
+// Called by all 256 threads; finds the grid's number `at` (s = -1: none).  The
+// chunks' size is that of `target` equal ones, at least kKaChunkMin.  Every
+// sequence counts, a bad length as one block.
+__device__ __forceinline__ KaChunk find_chunk(const Kv8View& kv, int batch, int target, int at) {
+  __shared__ int sum[8], found[4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int PER = kKaMaxChunkBatch / 256;  // sequences of a thread, consecutive
+  int m[PER], mine = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int s = tid * PER + k;
+    m[k] = 0;
+    if (s < batch) {
+      const int L = kv.seq_lens[s];
+      const bool bad = L < 1 || static_cast<long long>(L) > static_cast<long long>(kv.blocks) * kBlock;
+      m[k] = bad ? 1 : (L - 1) / kBlock + 1;
+    }
+    mine += m[k];
+  }
+  const auto scan = [&](int v, int& before) {  // sum over the CTA, and over the threads before this one
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) sum[warp] = inc;
+    __syncthreads();
+    int base = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      base += w < warp ? sum[w] : 0;
+      all += sum[w];
+    }
+    __syncthreads();
+    before = base + inc - v;
+    return all;
+  };
+  KaChunk c{};
+  int before = 0;
+  const long long tiles = static_cast<long long>(scan(mine, before)) * kv.hkv;
+  c.size = static_cast<int>(max(static_cast<long long>(kKaChunkMin), (tiles + target - 1) / target));
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) n += (m[k] + c.size - 1) / c.size;
+  (void)scan(n, before);
+  if (tid == 0) found[0] = -1;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int chunks = (m[k] + c.size - 1) / c.size, first = before * kv.hkv;
+    if (at >= first && at < first + chunks * kv.hkv) {
+      found[0] = tid * PER + k;
+      found[1] = (at - first) / chunks;
+      found[2] = (at - first) % chunks;
+      found[3] = chunks;
+    }
+    before += chunks;
+  }
+  __syncthreads();
+  c.s = found[0];
+  c.h = found[1];
+  c.q = found[2];
+  c.chunks = found[3];
+  return c;
+}
+
+// Partial sums of one chunk in the workspace: [G][128] o, [8] m, [8] l, flag.
+__device__ __forceinline__ size_t chunk_floats(int G) { return static_cast<size_t>(G) * kDim + 2 * kMaxGroup + 4; }
+
+template <int CODE, bool F32OUT, bool CHUNKS>
 __global__ void __launch_bounds__(256, 2)
     kv8_attend_kernel(const __grid_constant__ Kv8AttendParams p) {
   // the warps' rings; once every block is used, the warps' partials
@@ -576,26 +663,39 @@ __global__ void __launch_bounds__(256, 2)
   __shared__ float ml[kKaMaxWarps][2][kMaxGroup];
   __shared__ float cta_ml[2][kMaxGroup];
   __shared__ int cta_bad;
-  const int CS = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);
-  const int pair = static_cast<int>(blockIdx.y);
-  const int s = pair / p.kv.hkv, h = pair - s * p.kv.hkv;
+  const int CS = CHUNKS ? 1 : static_cast<int>(gridDim.x), rank = CHUNKS ? 0 : static_cast<int>(blockIdx.x);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int threads = static_cast<int>(blockDim.x), n_warps = threads >> 5;
   const int G = p.G;
-  // this warp's group among all of the cluster's
-  const int NG = CS * (n_warps >> 2), grp = rank * (n_warps >> 2) + (warp >> 2), quarter = warp & 3;
+  const int quarter = warp & 3;
   griddep_launch_dependents();
   griddep_wait();
 
-  // ---- the list.  Entries grp, grp + NG, .. below m - 1 are this group's
-  // stored blocks; lane l holds block, tile and scales of a chunk's l-th.  The
+  KaChunk ch{};
+  int pair, s, h;
+  if constexpr (CHUNKS) {
+    ch = find_chunk(p.kv, p.batch, p.target, static_cast<int>(blockIdx.x));
+    if (ch.s < 0) return;  // more CTAs than chunks
+    s = ch.s;
+    h = ch.h;
+    pair = s * p.kv.hkv + h;
+  } else {
+    pair = static_cast<int>(blockIdx.y);
+    s = pair / p.kv.hkv;
+    h = pair - s * p.kv.hkv;
+  }
+
+  // ---- the list.  Stored blocks of this warp's group: entries jb, jb + js, ..
+  // (n of them); lane l holds block, tile and scales of a chunk's l-th.  The
   // first chunk's block numbers are read together with the length and the count
   // (inside the list's storage whatever those turn out to be).
-  const int32_t* sel = p.sel_idx != nullptr ? p.sel_idx + static_cast<size_t>(pair) * p.max_sel : nullptr;
+  const int32_t* sel = !CHUNKS && p.sel_idx != nullptr ? p.sel_idx + static_cast<size_t>(pair) * p.max_sel : nullptr;
+  const int js = CS * (n_warps >> 2), grp = rank * (n_warps >> 2) + (warp >> 2);
+  const int jb = CHUNKS ? ch.q * ch.size + grp : grp;
   const int L = p.kv.seq_lens[s];
   int m = 0, first_b = 0, first_next = 0, last_b = 0;
-  const int first_j = grp + NG * lane;
   if (sel != nullptr) {
+    const int first_j = jb + js * lane;
     m = p.sel_count[pair];
     if (first_j < p.max_sel) first_b = sel[first_j];
     if (first_j + 1 < p.max_sel) first_next = sel[first_j + 1];
@@ -615,7 +715,8 @@ __global__ void __launch_bounds__(256, 2)
     if (m < 1 || m > p.max_sel) bad = true;
     if (!bad) last_b = sel[m - 1];
   }
-  int n = bad || grp >= m - 1 ? 0 : (m - 2 - grp) / NG + 1;
+  const int je = CHUNKS ? min(m - 1, (ch.q + 1) * ch.size) : m - 1;  // end of this CTA's (cluster's) stored entries
+  int n = bad || jb >= je ? 0 : (je - 1 - jb) / js + 1;
 
   int tile_c = 0, tile_n = 0;
   float ks_c = 0.f, vs_c = 0.f, ks_n = 0.f, vs_n = 0.f;
@@ -624,7 +725,7 @@ __global__ void __launch_bounds__(256, 2)
     bool ok = true;
     tile = 0;
     if (i < n) {
-      const int j = grp + NG * i;
+      const int j = jb + js * i;
       const int b = sel == nullptr ? j : (i0 == 0 ? first_b : sel[j]);
       if (sel != nullptr && (i0 == 0 ? first_next : sel[j + 1]) <= b) ok = false;  // ascending, so all lie below c
       const long long at = b < c ? p.kv.tile(s, h, b) : -1;
@@ -696,7 +797,8 @@ __global__ void __launch_bounds__(256, 2)
 
   // ---- the current block: the group whose turn it is, while its ring fills
   if (sel != nullptr && last_b != c) bad = true;
-  if (!bad && grp == (m - 1) % NG && 16 * quarter < L - c * kBlock) {
+  const bool tail_turn = CHUNKS ? (ch.q == ch.chunks - 1 && grp == 0) : grp == (m - 1) % js;
+  if (!bad && tail_turn && 16 * quarter < L - c * kBlock) {
     const size_t off = static_cast<size_t>(pair) * (kBlock * kDim);
     attend_tail(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * quarter, L - c * kBlock, p.scale_log2);
   }
@@ -770,6 +872,28 @@ __global__ void __launch_bounds__(256, 2)
     else
       static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
   };
+  if constexpr (CHUNKS) {
+    __syncthreads();
+    if (ch.chunks == 1) {
+      for (int i = tid; i < G * kDim; i += threads) {
+        const int hd = i / kDim, d = i % kDim;
+        store(hd, d, bad ? 0.f : part[(hd >> 1) * kKaHeadPair + (hd & 1) * kDim + d] / cta_ml[1][hd]);
+      }
+      if (bad && tid == 0) raise_status(p.status, kStatusBounds);
+    } else {
+      float* dst = p.ws_part + static_cast<size_t>(blockIdx.x) * chunk_floats(G);
+      for (int i = tid; i < G * kDim; i += threads) {
+        const int hd = i / kDim, d = i % kDim;
+        dst[i] = part[(hd >> 1) * kKaHeadPair + (hd & 1) * kDim + d];
+      }
+      if (tid < G) {
+        dst[G * kDim + tid] = cta_ml[0][tid];
+        dst[G * kDim + kMaxGroup + tid] = cta_ml[1][tid];
+      }
+      if (tid == 0) dst[G * kDim + 2 * kMaxGroup] = bad ? 1.f : 0.f;
+    }
+    return;
+  }
   // every CTA's partial is complete and visible to the cluster
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const int dpc = kDim / CS;
@@ -795,6 +919,75 @@ __global__ void __launch_bounds__(256, 2)
   if (any_bad && rank == 0 && tid == 0) raise_status(p.status, kStatusBounds);
   // no CTA leaves while another may still read its shared memory
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Merges the chunks' partial sums: one CTA per (sequence, KV head, query head of
+// the group), every thread one dimension of every second chunk, in order.
+template <bool F32OUT>
+__global__ void __launch_bounds__(256) kv8_combine_kernel(const __grid_constant__ Kv8AttendParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ float red[8], half_o[kDim];
+  __shared__ int first_s;
+  const int pair = static_cast<int>(blockIdx.x), s = pair / p.kv.hkv, h = pair - s * p.kv.hkv;
+  const int hd = static_cast<int>(blockIdx.y);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = p.G;
+  // the same cut as the first kernel's: a pair's chunks are consecutive
+  const int size = find_chunk(p.kv, p.batch, p.target, -1).size;
+  const auto chunks_of = [&](int k) {
+    const int L = p.kv.seq_lens[k];
+    const bool bad = L < 1 || static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
+    return ((bad ? 1 : (L - 1) / kBlock + 1) + size - 1) / size;
+  };
+  const int chunks = chunks_of(s);
+  if (chunks == 1) return;  // written by the first kernel
+  int before = 0;           // chunks of the sequences ahead
+  for (int k = tid; k < s; k += 256) before += chunks_of(k);
+  if (tid == 0) first_s = 0;
+  __syncthreads();
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0 && before > 0) atomicAdd(&first_s, before);  // integers: any order
+  __syncthreads();
+  const size_t stride = chunk_floats(G);
+  const float* src = p.ws_part + (static_cast<size_t>(first_s) * p.kv.hkv + static_cast<size_t>(h) * chunks) * stride;
+  const float *ms = src + G * kDim + hd, *ls = ms + kMaxGroup, *flag = src + G * kDim + 2 * kMaxGroup;
+  bool bad = false;
+  float top = -INFINITY;
+  for (int q = tid; q < chunks; q += 256) {
+    top = fmaxf(top, ms[q * stride]);
+    bad = bad || flag[q * stride] != 0.f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) red[warp] = top;
+  bad = __syncthreads_or(bad) != 0;
+  top = red[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) top = fmaxf(top, red[w]);
+  const int d = tid & (kDim - 1), half = tid >> 7;
+  const float* os = src + hd * kDim + d;
+  float o = 0.f, l = 0.f;
+#pragma unroll 8
+  for (int q = half; q < chunks; q += 2) {
+    const float f = weight(ms[q * stride], top);
+    o = fmaf(f, os[q * stride], o);
+    l = fmaf(f, ls[q * stride], l);
+  }
+  __syncthreads();  // red is read
+  if (half == 1) {
+    half_o[d] = o;
+    if (d == 0) red[0] = l;
+  }
+  __syncthreads();
+  if (half == 0) {
+    const float v = bad ? 0.f : (o + half_o[d]) / (l + red[0]);
+    const size_t at = (static_cast<size_t>(s) * p.hq + static_cast<size_t>(h) * G + hd) * kDim + d;
+    if constexpr (F32OUT)
+      static_cast<float*>(p.out)[at] = v;
+    else
+      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  }
+  if (bad && tid == 0) raise_status(p.status, kStatusBounds);
 }
 
 // ---------------------------------------------------------------- launches
@@ -844,7 +1037,7 @@ cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int 
 // the whole grid resident at once (2 x 148), up to one block a group.
 // Measured, (CTAs a cluster, groups) -> us: 64 pairs x 32 blocks (8, 1) 14.0,
 // (8, 2) 20.8, (4, 2) 11.7, (2, 2) 13.8; 256 pairs x 64 blocks (8, 1) 72.7,
-// (2, 2) 60.2, (1, 2) 53.4; 16 pairs x 2,000 blocks (8, 2) 114, (16, 2) 105.
+// (2, 2) 60.2, (1, 2) 53.4.
 Kv8AttendPlan kv8_attend_plan(int pairs, int max_blocks) {
   Kv8AttendPlan a{};
   a.groups = 2;
@@ -854,25 +1047,51 @@ Kv8AttendPlan kv8_attend_plan(int pairs, int max_blocks) {
   return a;
 }
 
-cudaError_t launch_kv8_attend(int code, bool f32_out, const Kv8AttendParams& p, int batch, cudaStream_t stream) {
-  const int pairs = batch * p.kv.hkv;
+// The grid holds target + pairs chunks at most.  Up to 74 pairs they all fit
+// the GPU at once (2 x 148 CTAs); more pairs have no use for a single wave.
+static int chunk_target(int pairs) { return pairs <= 74 ? 2 * 148 - pairs : 4 * 148; }
+
+size_t kv8_attend_scratch_bytes(int pairs, int G) {
+  return static_cast<size_t>(chunk_target(pairs) + pairs) * (static_cast<size_t>(G) * kDim + 2 * kMaxGroup + 4) * 4;
+}
+
+cudaError_t launch_kv8_attend(int code, bool f32_out, Kv8AttendParams p, cudaStream_t stream) {
+  const int pairs = p.batch * p.kv.hkv;
+  // Chunks where a sequence may be longer than a few of them and the workspace
+  // holds their partial sums
+  if (p.sel_idx == nullptr && p.ws_part != nullptr && p.batch <= kKaMaxChunkBatch && p.kv.blocks > 4 * kKaChunkMin) {
+    constexpr size_t smem = kKaMaxWarps * std::max(kKaStages * kKaSlot, kKaPart * 4);
+    p.target = chunk_target(pairs);
+    const dim3 grid(static_cast<unsigned>(p.target + pairs)), cgrid(static_cast<unsigned>(pairs), static_cast<unsigned>(p.G));
+    cudaError_t e;
+    if (code == kCodeE4m3)
+      e = f32_out ? launch(kv8_attend_kernel<kCodeE4m3, true, true>, grid, 256, smem, 0, stream, p)
+                  : launch(kv8_attend_kernel<kCodeE4m3, false, true>, grid, 256, smem, 0, stream, p);
+    else
+      e = f32_out ? launch(kv8_attend_kernel<kCodeInt8, true, true>, grid, 256, smem, 0, stream, p)
+                  : launch(kv8_attend_kernel<kCodeInt8, false, true>, grid, 256, smem, 0, stream, p);
+    if (e != cudaSuccess) return e;
+    return f32_out ? launch(kv8_combine_kernel<true>, cgrid, 256, 0, 0, stream, p)
+                   : launch(kv8_combine_kernel<false>, cgrid, 256, 0, 0, stream, p);
+  }
   const Kv8AttendPlan a = kv8_attend_plan(pairs, p.sel_idx != nullptr ? p.max_sel : p.kv.blocks);
   const dim3 grid(static_cast<unsigned>(a.cluster), static_cast<unsigned>(pairs));
   const int T = 128 * a.groups;
   const size_t smem = static_cast<size_t>(4 * a.groups) * std::max(kKaStages * kKaSlot, kKaPart * 4);
   if (code == kCodeE4m3)
-    return f32_out ? launch(kv8_attend_kernel<kCodeE4m3, true>, grid, T, smem, a.cluster, stream, p)
-                   : launch(kv8_attend_kernel<kCodeE4m3, false>, grid, T, smem, a.cluster, stream, p);
-  return f32_out ? launch(kv8_attend_kernel<kCodeInt8, true>, grid, T, smem, a.cluster, stream, p)
-                 : launch(kv8_attend_kernel<kCodeInt8, false>, grid, T, smem, a.cluster, stream, p);
+    return f32_out ? launch(kv8_attend_kernel<kCodeE4m3, true, false>, grid, T, smem, a.cluster, stream, p)
+                   : launch(kv8_attend_kernel<kCodeE4m3, false, false>, grid, T, smem, a.cluster, stream, p);
+  return f32_out ? launch(kv8_attend_kernel<kCodeInt8, true, false>, grid, T, smem, a.cluster, stream, p)
+                 : launch(kv8_attend_kernel<kCodeInt8, false, false>, grid, T, smem, a.cluster, stream, p);
 }
 
 cudaError_t prepare_kv8_kernels() {
   constexpr int smem = kKaMaxWarps * std::max(kKaStages * kKaSlot, kKaPart * 4);
-  for (auto* k : {kv8_attend_kernel<kCodeE4m3, false>, kv8_attend_kernel<kCodeE4m3, true>,
-                  kv8_attend_kernel<kCodeInt8, false>, kv8_attend_kernel<kCodeInt8, true>}) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (auto* k : {kv8_attend_kernel<kCodeE4m3, false, false>, kv8_attend_kernel<kCodeE4m3, true, false>,
+                  kv8_attend_kernel<kCodeInt8, false, false>, kv8_attend_kernel<kCodeInt8, true, false>,
+                  kv8_attend_kernel<kCodeE4m3, false, true>, kv8_attend_kernel<kCodeE4m3, true, true>,
+                  kv8_attend_kernel<kCodeInt8, false, true>, kv8_attend_kernel<kCodeInt8, true, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

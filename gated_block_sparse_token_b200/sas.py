@@ -116,6 +116,7 @@ def lib() -> ctypes.CDLL:
             "sas_kv8_append": (ctypes.c_int, [cfgp, kv8p, rwp, rwp, vp, vp, i32, vp, sz, vp]),
             "sas_kv8_read": (ctypes.c_int, [cfgp, kv8p, vp, i32, rwp, rwp, vp, sz, vp]),
             "sas_pool_keys_kv8": (ctypes.c_int, [cfgp, kv8p, vp, i32, vp, vp, vp, i32, vp, vp, sz, vp]),
+            "sas_sparse_decode_kv8_workspace_bytes": (sz, [cfgp, i32]),
             "sas_sparse_decode_kv8": (ctypes.c_int, [cfgp, vp, kv8p, vp, vp, vp, vp, sz, vp]),
             "sas_prefill_gate_backward": (ctypes.c_int, [cfgp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp,
                                                          vp, vp, vp, vp, vp, sz, vp]),
@@ -620,9 +621,15 @@ def pool_keys_kv8(cfg: Config, kv: KvCache8, w_k, gamma_k, gate_keys, ws, blk_be
            "sas_pool_keys_kv8")
 
 
+def sparse_decode_kv8_workspace_bytes(cfg: Config, batch: int) -> int:
+    return int(lib().sas_sparse_decode_kv8_workspace_bytes(ctypes.byref(_config(cfg)), batch))
+
+
 def sparse_decode_kv8(cfg: Config, q, kv: KvCache8, sel_idx, sel_count, out, ws, stream=None) -> None:
     """sas_sparse_decode_kv8: q bf16 [B][Hq][128], out cfg.out_dtype likewise;
-    sel_idx / sel_count as topk_blocks writes them, or both None: every block."""
+    sel_idx / sel_count as topk_blocks writes them, or both None: every block
+    (then with sparse_decode_kv8_workspace_bytes(cfg, B) bytes of ws, few or
+    ragged long sequences use the whole GPU)."""
     B, hkv = kv.batch, cfg.num_kv_heads
     _plain("q", q, (B, cfg.num_q_heads, 128), torch.bfloat16)
     _plain("out", out, (B, cfg.num_q_heads, 128), out_dtype(cfg))

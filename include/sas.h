@@ -594,6 +594,11 @@ SAS_API sas_status sas_pool_keys_kv8(const sas_config* cfg, const sas_kv8* kv,
                                      int32_t max_gate_blocks, float* pooled_raw, void* ws,
                                      size_t ws_bytes, sas_stream_t stream);
 
+/* Bytes of workspace with which sas_sparse_decode_kv8 over every block divides
+ * few or ragged long sequences over the whole GPU (their partial sums live
+ * there); for a given configuration the largest batch of the calls counts. */
+SAS_API size_t sas_sparse_decode_kv8_workspace_bytes(const sas_config* cfg, int32_t batch);
+
 /*
  * sas_sparse_decode over the 8-bit cache: softmax attention of one query token
  * per sequence over the listed blocks, the stored ones as code * scale and the
@@ -602,6 +607,10 @@ SAS_API sas_status sas_pool_keys_kv8(const sas_config* cfg, const sas_kv8* kv,
  *   sel_idx [B][Hkv][budget/64], sel_count [B][Hkv]: as for sas_sparse_decode;
  *        both NULL: every block of the sequence (dense attention, any length)
  *   out  out_dtype [B][Hq][128]
+ *   ws   at least sas_workspace_bytes(cfg, 0, 0); with at least
+ *        sas_sparse_decode_kv8_workspace_bytes(cfg, B), attention over every
+ *        block is cut into equal chunks that a second kernel merges (calls that
+ *        may overlap on the GPU then need a workspace each)
  * Logits, softmax statistics and sums are fp32.  The probabilities enter the
  * product with the values as f16 (a bf16 output) or as the sum of two f16
  * terms (an fp32 output).  kv_dtype must be bf16; the gated mode is refused

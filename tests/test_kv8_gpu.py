@@ -310,6 +310,49 @@ def test_attend_every_block(code, paged, lens):
     check_attend(kv, cfg, 3, None, q, o, lens)
 
 
+def chunk_ws(cfg, B):
+    return torch.full((sas.sparse_decode_kv8_workspace_bytes(cfg, B),), 0, dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[30001], [20000, 1, 64, 9000, 65], [4097, 4096, 4095], [70000, 33]])
+def test_attend_every_block_in_chunks(code, out, lens):
+    """With the larger workspace: few and ragged sequences cut into chunks; left-over contents of the workspace do
+    not matter, and two calls agree bit for bit."""
+    cfg = sas.Config(6, 2, out_dtype=out)
+    kv = K.make_cache(len(lens), 2, (max(lens) + 63) // 64, code, len(lens) != 3, lens, DEV, seed=3)
+    ws = chunk_ws(cfg, len(lens))
+    ws[256:] = 255
+    q, o = run_attend(kv, cfg, 3, None, ws)
+    assert ok(ws)
+    check_attend(kv, cfg, 3, None, q, o, lens)
+    o2 = run_attend(kv, cfg, 3, None, ws)[1]
+    assert torch.equal(o, o2)
+
+
+def test_attend_chunks_many_short_sequences_and_bad_ones():
+    """More sequences than a warp, most of them short, some with lengths or pages out of range."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(1, 200, (300,), generator=g).tolist()
+    lens[7], lens[299] = 5000, 4800
+    cfg = sas.Config(2, 1)
+    kv = K.make_cache(300, 1, 80, K.E4M3, True, lens, DEV, seed=4, spare=1)
+    ws = chunk_ws(cfg, 300)
+    kv.seq_lens[11] = 0
+    kv.seq_lens[12] = 80 * 64 + 1
+    kv.block_table[299, 3] = -1
+    q, o = run_attend(kv, cfg, 2, None, ws)
+    torch.cuda.synchronize()
+    assert sas.get_device_status(ws) == sas.SAS_ERR_DEVICE_BOUNDS
+    bad = {11, 12, 299}
+    for s in bad:
+        assert float(o[s].float().abs().max()) == 0
+    for s in [0, 7, 10, 13, 150, 255, 256, 298]:
+        want, size = K.attend(kv, q, s, 0, 2, list(range((lens[s] - 1) // 64 + 1)), lens[s], cfg.attn_scale)
+        assert bool(((o[s].cpu().double() - want).abs() <= 2.0 ** -10 * size + 2.0 ** -8 * want.abs()).all()), s
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -120, 1e-20, 1.0, 1e15])
 def test_attend_query_range(scale):
     """The query is brought into f16's range by a power of two per head: only attn_scale * q counts."""
