@@ -35,10 +35,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------- write
-// One CTA per (block job, KV head, sequence): threads 0-127 the keys, 128-255
-// the values, 8 rows x 8 dims per thread in registers between the maximum and
-// the rounding, so a block is read once and its codes written once.  Job 0 also
-// writes the tail, after its block has read the tail's old rows.
+// A CTA walks every gridDim.x-th block that the append completes for one
+// (sequence, KV head): threads 0-127 the keys, 128-255 the values, 8 rows x 8
+// dims per thread in registers between the maximum and the rounding, so a block
+// is read once and its codes written once; the next block's loads go out as
+// soon as the codes are made.  CTA 0 also writes the tail, after its first block
+// has read the tail's old rows.
 __device__ __forceinline__ uint4 load_new_row(const RowsView& r, long long tok, int h, int s, int d0) {
   const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(r.data) + static_cast<long long>(s) * r.seq +
                            tok * r.token + static_cast<long long>(h) * r.head + d0;
@@ -46,7 +48,7 @@ __device__ __forceinline__ uint4 load_new_row(const RowsView& r, long long tok, 
 }
 
 template <int CODE>
-__global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
+__global__ void __launch_bounds__(256, 3) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int s = blockIdx.z, h = blockIdx.y;
@@ -63,9 +65,8 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
   __nv_bfloat16* tail = const_cast<__nv_bfloat16*>(half == 0 ? p.kv.k_tail : p.kv.v_tail) +
                         (static_cast<long long>(s) * p.kv.hkv + h) * (kBlock * kDim);
   const int d0 = 8 * (tid & 15), r0 = tid >> 4;  // 16 lanes a row, rows r0, r0 + 8, ..
-  const int b = b_first + static_cast<int>(blockIdx.x);
   uint4 x[8];
-  if (b < b_done) {  // never when err; the rows lie in the input and the tail whatever the pages are
+  const auto load_block = [&](int b) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int row = r0 + 8 * i;
@@ -73,17 +74,20 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
       x[i] = t < 0 ? *reinterpret_cast<const uint4*>(tail + row * kDim + d0)
                    : load_new_row(src, start + t, h, s, d0);
     }
-  }
+  };
+  int b = b_first + static_cast<int>(blockIdx.x);
+  // never when err; the rows lie in the input and the tail whatever the pages are
+  if (b < b_done) load_block(b);
   // a page out of range anywhere in the write skips the whole (sequence, head)
   if (p.kv.block_table != nullptr)
     for (int k = b_first + static_cast<int>(threadIdx.x); k < b_done; k += 256)
       if (p.kv.tile(s, h, k) < 0) err = true;
-  __shared__ uint32_t amax_s[2][4];
+  __shared__ uint32_t amax_s[2][2][4];  // by the parity of the round: one barrier a block
   if (__syncthreads_or(err)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(p.status, kStatusBounds);
     return;
   }
-  if (b < b_done) {
+  for (int round = 0; b < b_done; b += static_cast<int>(gridDim.x), ++round) {
     uint32_t m = 0;  // two bf16 magnitudes
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -92,9 +96,10 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
     }
     m = max(m & 0xffffu, m >> 16);
     m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) amax_s[half][tid >> 5] = m;
+    uint32_t* am = amax_s[round & 1][half];
+    if (lane == 0) am[tid >> 5] = m;
     __syncthreads();
-    m = max(max(amax_s[half][0], amax_s[half][1]), max(amax_s[half][2], amax_s[half][3]));
+    m = max(max(am[0], am[1]), max(am[2], am[3]));
     const bool finite = m < kBf16Inf;
     const uint32_t abits = finite ? max(m << 16, kMinAmaxBits) : 0x3f800000u;
     const float a = __uint_as_float(abits);
@@ -108,12 +113,11 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
     const float pw = __uint_as_float(((255u - (abits >> 23)) << 23));
     const float an = a * pw, inv = 1.f / an;
     const float R = qmax / an * pw, T = qmax * pw;
-    const long long tile = p.kv.tile(s, h, b);
-    uint8_t* dst = const_cast<uint8_t*>(half == 0 ? p.kv.k : p.kv.v) + tile * kTile8Bytes;
-    auto quot = [&](float v) {
+    const auto quot = [&](float v) {
       const float q = v * R;
       return fmaf(fmaf(-q, an, v * T), inv, q);
     };
+    uint2 code[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -125,13 +129,21 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
         if constexpr (CODE == kCodeE4m3) {
           c[k] = static_cast<uint32_t>(cvt_e4m3x2(y0, y1)) | (static_cast<uint32_t>(cvt_e4m3x2(y2, y3)) << 16);
         } else {
-          const uint32_t i0 = __float2int_rn(y0) & 0xff, i1 = __float2int_rn(y1) & 0xff;
-          const uint32_t i2 = __float2int_rn(y2) & 0xff, i3 = __float2int_rn(y3) & 0xff;
-          c[k] = i0 | (i1 << 8) | (i2 << 16) | (i3 << 24);
+          // y + 1.5 * 2^23 rounds y to the nearest integer (even on a tie) in
+          // its low bits, whose low byte is the code
+          constexpr float magic = 12582912.f;
+          const uint32_t p01 = __byte_perm(__float_as_uint(y0 + magic), __float_as_uint(y1 + magic), 0x0040);
+          const uint32_t p23 = __byte_perm(__float_as_uint(y2 + magic), __float_as_uint(y3 + magic), 0x0040);
+          c[k] = __byte_perm(p01, p23, 0x5410);
         }
       }
-      *reinterpret_cast<uint2*>(dst + (r0 + 8 * i) * kDim + d0) = finite ? make_uint2(c[0], c[1]) : make_uint2(0u, 0u);
+      code[i] = finite ? make_uint2(c[0], c[1]) : make_uint2(0u, 0u);
     }
+    if (b + static_cast<int>(gridDim.x) < b_done) load_block(b + static_cast<int>(gridDim.x));
+    const long long tile = p.kv.tile(s, h, b);
+    uint8_t* dst = const_cast<uint8_t*>(half == 0 ? p.kv.k : p.kv.v) + tile * kTile8Bytes;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint2*>(dst + (r0 + 8 * i) * kDim + d0) = code[i];
     if (tid == 0)
       const_cast<float*>(half == 0 ? p.kv.k_scale : p.kv.v_scale)[tile] =
           finite ? __fdiv_rn(a, qmax) : __uint_as_float(0x7fc00000u);
@@ -147,26 +159,17 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------- read-back
-// One CTA per (64 output tokens, KV head, sequence), threads 0-127 the keys,
-// 128-255 the values; 8 lanes a row, 16 codes a lane, four rows a thread whose
-// loads go out together.  The 64 tokens lie in two blocks at most.
-template <typename OutT>
-__device__ __forceinline__ void store16(OutT* dst, const float (&x)[16]) {
-  if constexpr (std::is_same_v<OutT, float>) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      reinterpret_cast<float4*>(dst)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      reinterpret_cast<uint4*>(dst)[k] =
-          make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
-                     pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
-  }
-}
-
+// A CTA walks every gridDim.x-th block of one (sequence, KV head)'s range,
+// threads 0-127 the keys, 128-255 the values.  A lane turns as many codes as
+// make 16 output bytes, so that a warp's stores fill whole sectors; the next
+// block's codes are requested before this one's values are stored.
 template <int CODE, typename OutT>
-__global__ void __launch_bounds__(256, 5) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
+__global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
+  constexpr int VEC = 16 / static_cast<int>(sizeof(OutT));  // codes of a lane: 8 or 4
+  constexpr int LPR = kDim / VEC;                           // lanes of a row
+  constexpr int ROWS = 128 / LPR;                           // rows of a pass: 8 or 4
+  constexpr int N = kBlock / ROWS;                          // passes
+  using Codes = std::conditional_t<VEC == 8, uint2, uint32_t>;
   griddep_launch_dependents();
   griddep_wait();
   const int s = blockIdx.z, h = blockIdx.y;
@@ -175,78 +178,86 @@ __global__ void __launch_bounds__(256, 5) kv8_read_kernel(const __grid_constant_
   const int begin = p.begin != nullptr ? p.begin[s] : 0;
   const RowsView o = half == 0 ? p.k_out : p.v_out;
   bool err = L < 1 || begin < 0 || static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
-  // tokens of this CTA: positions first .. first + n - 1
-  const int t0 = static_cast<int>(blockIdx.x) * kBlock;
-  const long long first = static_cast<long long>(begin) + t0;
-  const int n = err ? 0 : static_cast<int>(min(static_cast<long long>(min(kBlock, p.count - t0)), L - first));
-  if (o.data != nullptr && n > 0) {
-    const int c = (L - 1) / kBlock, b0 = static_cast<int>(first / kBlock), off = static_cast<int>(first % kBlock);
+  // positions begin .. end - 1, in blocks b0 .. b1 - 1
+  const int end = err ? 0 : static_cast<int>(min(static_cast<long long>(begin) + p.count, static_cast<long long>(L)));
+  if (o.data != nullptr && begin < end) {
+    const int c = (L - 1) / kBlock, b0 = begin / kBlock, b1 = (end - 1) / kBlock + 1, step = static_cast<int>(gridDim.x);
     const uint8_t* codes = half == 0 ? p.kv.k : p.kv.v;
     const float* scales = half == 0 ? p.kv.k_scale : p.kv.v_scale;
-    // the two blocks: tile and scale (scale 0 and tile -1: a page out of range)
-    long long tile0 = -1, tile1 = -1;
-    float sc0 = 0.f, sc1 = 0.f;
-    if (b0 < c) {
-      tile0 = p.kv.tile(s, h, b0);
-      if (tile0 >= 0) sc0 = scales[tile0];
-      if (tile0 < 0) err = true;
-    }
-    if (b0 + 1 < c && off + n > kBlock) {
-      tile1 = p.kv.tile(s, h, b0 + 1);
-      if (tile1 >= 0) sc1 = scales[tile1];
-      if (tile1 < 0) err = true;
-    }
-    const int d0 = 16 * (tid & 7), r0 = tid >> 3;  // rows r0, r0 + 16, ..
+    const int d0 = VEC * (tid % LPR), r0 = tid / LPR;  // rows r0, r0 + ROWS, ..
     OutT* out = static_cast<OutT*>(const_cast<void*>(o.data)) + static_cast<long long>(s) * o.seq +
-                static_cast<long long>(h) * o.head + static_cast<long long>(t0) * o.token + d0;
-    uint4 w[4];
+                static_cast<long long>(h) * o.head + d0;
+    const auto store = [&](int pos, const float (&x)[VEC]) {
+      if (pos < begin || pos >= end) return;
+      OutT* dst = out + static_cast<long long>(pos - begin) * o.token;
+      if constexpr (VEC == 4)
+        *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+      else
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                    pack_bf16x2(x[4], x[VEC - 3]), pack_bf16x2(x[VEC - 2], x[VEC - 1]));
+    };
+    Codes w[N];
+    float sc = 0.f;
+    long long tile = -1, tile_n = -1;
+    const int be = min(b1, c);  // the stored ones
+    const auto load_block = [&]() {
+      if (tile < 0) return;
+      sc = scales[tile];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = r0 + 16 * i, at = off + t;
-      const long long tile = at < kBlock ? tile0 : tile1;
-      w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (t < n && tile >= 0)
-        w[i] = *reinterpret_cast<const uint4*>(codes + tile * kTile8Bytes + (at & (kBlock - 1)) * kDim + d0);
+      for (int i = 0; i < N; ++i)
+        w[i] = *reinterpret_cast<const Codes*>(codes + tile * kTile8Bytes + (r0 + ROWS * i) * kDim + d0);
+    };
+    int b = b0 + static_cast<int>(blockIdx.x);
+    if (b < be) {
+      tile = p.kv.tile(s, h, b);
+      if (b + step < be) tile_n = p.kv.tile(s, h, b + step);
+      load_block();
     }
+    for (; b < be; b += step) {
+      Codes cur[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = r0 + 16 * i, at = off + t;
-      if (t >= n || b0 + (at >= kBlock) >= c) continue;  // past the end, or the current block (below)
-      const float sc = at < kBlock ? sc0 : sc1;
-      const bool known = (at < kBlock ? tile0 : tile1) >= 0;
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      float x[16];
+      for (int i = 0; i < N; ++i) cur[i] = w[i];
+      const float cur_sc = sc;
+      const bool known = tile >= 0;
+      if (!known) err = true;
+      tile = tile_n;
+      if (b + step < be) load_block();
+      if (b + 2 * step < be) tile_n = p.kv.tile(s, h, b + 2 * step);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t lo, hi;
-        codes_f16<CODE>(u[k], lo, hi);
-        x[4 * k] = f16_lo(lo) * sc;
-        x[4 * k + 1] = f16_hi(lo) * sc;
-        x[4 * k + 2] = f16_lo(hi) * sc;
-        x[4 * k + 3] = f16_hi(hi) * sc;
-      }
-      if (!known) {
+      for (int i = 0; i < N; ++i) {
+        float x[VEC];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = 0.f;
-      }
-      store16(out + static_cast<long long>(t) * o.token, x);
-    }
-    if (b0 + 1 >= c) {  // rows of the current block: from the tail
-      const __nv_bfloat16* tail = (half == 0 ? p.kv.k_tail : p.kv.v_tail) +
-                                  (static_cast<long long>(s) * p.kv.hkv + h) * (kBlock * kDim);
-      for (int t = r0; t < n; t += 16) {
-        const int at = off + t;
-        if (b0 + (at >= kBlock) != c) continue;
-        const uint4* v = reinterpret_cast<const uint4*>(tail + (at & (kBlock - 1)) * kDim + d0);
-        const uint4 v0 = v[0], v1 = v[1];
-        const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        float x[16];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          x[2 * k] = bf16_lo(u[k]);
-          x[2 * k + 1] = bf16_hi(u[k]);
+        for (int k = 0; k < VEC / 4; ++k) {
+          uint32_t lo, hi, word;
+          if constexpr (VEC == 8)
+            word = k == 0 ? cur[i].x : cur[i].y;
+          else
+            word = cur[i];
+          codes_f16<CODE>(word, lo, hi);
+          x[4 * k] = f16_lo(lo) * cur_sc;
+          x[4 * k + 1] = f16_hi(lo) * cur_sc;
+          x[4 * k + 2] = f16_lo(hi) * cur_sc;
+          x[4 * k + 3] = f16_hi(hi) * cur_sc;
         }
-        store16(out + static_cast<long long>(t) * o.token, x);
+        if (!known) {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) x[k] = 0.f;
+        }
+        store(b * kBlock + r0 + ROWS * i, x);
+      }
+    }
+    if (c < b1 && static_cast<int>(blockIdx.x) == (c - b0) % step) {  // the current block: from the tail
+      const __nv_bfloat16* tail = (half == 0 ? p.kv.k_tail : p.kv.v_tail) +
+                                  (static_cast<long long>(s) * p.kv.hkv + h) * (kBlock * kDim) + d0;
+      for (int row = r0; row < end - c * kBlock; row += ROWS) {
+        float x[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(tail + row * kDim + 2 * k);
+          x[2 * k] = bf16_lo(u);
+          x[2 * k + 1] = bf16_hi(u);
+        }
+        store(c * kBlock + row, x);
       }
     }
   }
@@ -1015,17 +1026,29 @@ cudaError_t launch(void (*k)(Args...), dim3 grid, int threads, size_t smem, int 
 
 }  // namespace
 
+// CTAs of one (sequence, head) that walk `blocks` blocks: four waves of three an
+// SM over all pairs (a ragged batch levels out), or about four blocks a CTA if
+// that makes more, at most one a block.  Read-back of 32 pairs x 513 blocks with
+// 37 / 55 / 111 CTAs a pair: 138 / 135 / 130 us; of 48 pairs x 129 with 25 / 37 /
+// 74: 31.6 / 30.1 / 31.4.
+static unsigned walkers(long long blocks, long long pairs) {
+  const long long n = std::max((148 * 12 + pairs - 1) / pairs, blocks / 4);
+  return static_cast<unsigned>(std::max<long long>(1, std::min(blocks, n)));
+}
+
 cudaError_t launch_kv8_append(int code, const Kv8AppendParams& p, int batch, cudaStream_t stream) {
   // at most (63 + max_new) / 64 blocks are completed
-  const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.max_new) + kBlock - 1) / kBlock),
-                  static_cast<unsigned>(p.kv.hkv), static_cast<unsigned>(batch));
+  const long long blocks = (static_cast<long long>(p.max_new) + kBlock - 1) / kBlock;
+  const dim3 grid(walkers(blocks, static_cast<long long>(batch) * p.kv.hkv), static_cast<unsigned>(p.kv.hkv),
+                  static_cast<unsigned>(batch));
   return code == kCodeE4m3 ? launch(kv8_append_kernel<kCodeE4m3>, grid, 256, 0, 0, stream, p)
                            : launch(kv8_append_kernel<kCodeInt8>, grid, 256, 0, 0, stream, p);
 }
 
 cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int batch, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.count) + kBlock - 1) / kBlock),
-                  static_cast<unsigned>(p.kv.hkv), static_cast<unsigned>(batch));
+  const long long blocks = (static_cast<long long>(p.count) + kBlock - 1) / kBlock + 1;
+  const dim3 grid(walkers(blocks, static_cast<long long>(batch) * p.kv.hkv), static_cast<unsigned>(p.kv.hkv),
+                  static_cast<unsigned>(batch));
   if (code == kCodeE4m3)
     return f32_out ? launch(kv8_read_kernel<kCodeE4m3, float>, grid, 256, 0, 0, stream, p)
                    : launch(kv8_read_kernel<kCodeE4m3, __nv_bfloat16>, grid, 256, 0, 0, stream, p);
