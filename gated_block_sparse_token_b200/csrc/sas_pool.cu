@@ -258,25 +258,25 @@ constexpr int kPpSmem = kPpA + kPpB + 2 * kPpRows * 4 + 64 + 1024;
 
 enum PoolSource : int { kSrcE4m3 = kCodeE4m3, kSrcInt8 = kCodeInt8, kSrcBf16 };
 
-// Pooled codes of dims 4 lane .. 4 lane + 3 over ROWS rows of a tile, the first
-// at src (the lane's four codes of it): maximum and minimum as f16 pairs (dims
-// 0, 1 and 2, 3), the sums in fp32 -- all exact (sums are multiples of 2^-9
-// below 2^15).  A lane reads its 4 bytes of every row, so nothing is left to
-// reduce across lanes.  int8 codes stay biased by 1152 until the end (exact
-// in f16): taking the bias off each would cost as much as the maxima.
-template <int CODE, int ROWS>
-__device__ __forceinline__ void pool_codes(const uint8_t* src, float (&mx)[4], float (&mn)[4], float (&sm)[4]) {
-  constexpr int STEP = ROWS < 32 ? ROWS : 32;  // rows in flight
-  uint32_t hx[2] = {0u, 0u}, hn[2] = {0u, 0u};
+// Pooled codes of dims 4 lane .. 4 lane + 3 (a lane's four codes of each row, so
+// that nothing is left to reduce across lanes): maximum and minimum as f16 pairs
+// (dims 0, 1 and 2, 3), the sums in fp32 -- all exact (sums are multiples of
+// 2^-9 below 2^15, or integers below 2^17).  int8 codes stay biased by 1152 until
+// the end (exact in f16): taking the bias off each would cost as much as the
+// maxima.
+template <int CODE>
+struct PooledCodes {
+  uint32_t hx[2], hn[2];
+  float sm[4];
+
+  template <int ROWS>
+  __device__ __forceinline__ void add(const uint32_t (&raw)[ROWS], bool first) {
+    if (first) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v) sm[v] = 0.f;
+      for (int v = 0; v < 4; ++v) sm[v] = 0.f;
+    }
 #pragma unroll
-  for (int r0 = 0; r0 < ROWS; r0 += STEP) {
-    uint32_t raw[STEP];
-#pragma unroll
-    for (int r = 0; r < STEP; ++r) raw[r] = *reinterpret_cast<const uint32_t*>(src + (r0 + r) * kDim);
-#pragma unroll
-    for (int r = 0; r < STEP; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
       uint32_t c[2];
       if constexpr (CODE == kCodeE4m3) {
         codes_f16<CODE>(raw[r], c[0], c[1]);
@@ -287,20 +287,30 @@ __device__ __forceinline__ void pool_codes(const uint8_t* src, float (&mx)[4], f
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        hx[k] = r0 + r == 0 ? c[k] : max_f16x2(hx[k], c[k]);
-        hn[k] = r0 + r == 0 ? c[k] : min_f16x2(hn[k], c[k]);
+        const bool init = first && r == 0;
+        hx[k] = init ? c[k] : max_f16x2(hx[k], c[k]);
+        hn[k] = init ? c[k] : min_f16x2(hn[k], c[k]);
         add_f16x2(sm[2 * k], sm[2 * k + 1], c[k]);
       }
     }
   }
-  constexpr float bias = CODE == kCodeInt8 ? 1152.f : 0.f;
+  // mx, mn, sm over all of `rows` rows
+  __device__ __forceinline__ void get(int rows, float (&mx)[4], float (&mn)[4], float (&s)[4]) const {
+    constexpr float bias = CODE == kCodeInt8 ? 1152.f : 0.f;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    mx[2 * k] = f16_lo(hx[k]) - bias, mx[2 * k + 1] = f16_hi(hx[k]) - bias;
-    mn[2 * k] = f16_lo(hn[k]) - bias, mn[2 * k + 1] = f16_hi(hn[k]) - bias;
+    for (int k = 0; k < 2; ++k) {
+      mx[2 * k] = f16_lo(hx[k]) - bias, mx[2 * k + 1] = f16_hi(hx[k]) - bias;
+      mn[2 * k] = f16_lo(hn[k]) - bias, mn[2 * k + 1] = f16_hi(hn[k]) - bias;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) s[v] = sm[v] - static_cast<float>(rows) * bias;
   }
+};
+
+template <int ROWS>
+__device__ __forceinline__ void load_codes(uint32_t (&raw)[ROWS], const uint8_t* src) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v) sm[v] -= ROWS * bias;
+  for (int r = 0; r < ROWS; ++r) raw[r] = *reinterpret_cast<const uint32_t*>(src + r * kDim);
 }
 
 // Threads of the kernel for a source: codes are pooled by sixteen warps (the
@@ -357,11 +367,26 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
   // ---- pooling into the A operand
   if constexpr (SRC != kSrcBf16) {
     bool err = false;
-    for (int i = warp; i < kPpRows; i += pp_threads(SRC) / 32) {  // warp-uniform
-      const long long row = row_of(i);
+    // a warp's blocks i, i + 16, ..: each in two halves of 32 rows, the next
+    // half's loads in flight while one is worked on, the next block's cache row
+    // known a block ahead
+    constexpr int STEP = pp_threads(SRC) / 32;
+    uint32_t r0[kBlock / 2], r1[kBlock / 2];
+    const uint8_t* kb = static_cast<const uint8_t*>(p.kv.k) + 4 * lane;
+    long long row = row_of(warp), row_n = row_of(warp + STEP);
+    // unconditional loads (tile 0 for a row that is not pooled): a load under a
+    // condition would be waited for where the paths meet
+    load_codes(r0, kb + max(row, 0ll) * kDim);
+    for (int i = warp; i < kPpRows; i += STEP) {  // warp-uniform
       if (row == -2) err = true;
+      const long long row_2n = i + 2 * STEP < kPpRows ? row_of(i + 2 * STEP) : -1;
       float mx[4] = {0.f, 0.f, 0.f, 0.f}, mn[4] = {0.f, 0.f, 0.f, 0.f}, sm[4] = {0.f, 0.f, 0.f, 0.f};
-      if (row >= 0) pool_codes<SRC, kBlock>(static_cast<const uint8_t*>(p.kv.k) + row * kDim + 4 * lane, mx, mn, sm);
+      PooledCodes<SRC> pool;
+      load_codes(r1, kb + (max(row, 0ll) + kBlock / 2) * kDim);
+      pool.add(r0, true);
+      load_codes(r0, kb + max(row_n, 0ll) * kDim);
+      pool.add(r1, false);
+      if (row >= 0) pool.get(kBlock, mx, mn, sm);
       uint32_t pk[4][2];
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
@@ -388,6 +413,8 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
           pr[2 * kDim + v] = sm[v] * (1.f / kBlock) * sc;
         }
       }
+      row = row_n;
+      row_n = row_2n;
     }
     if (err && lane == 0) raise_status(p.status, kStatusBounds);
   } else {
@@ -618,7 +645,11 @@ __global__ void __launch_bounds__(kPfThreads) pool_few_kernel(const __grid_const
   {
     constexpr int R = kBlock / kPfWarps;
     float mx[4], mn[4], sm[4];
-    pool_codes<CODE, R>(static_cast<const uint8_t*>(p.kv.k) + (row + R * warp) * kDim + 4 * lane, mx, mn, sm);
+    uint32_t raw[R];
+    load_codes(raw, static_cast<const uint8_t*>(p.kv.k) + (row + R * warp) * kDim + 4 * lane);
+    PooledCodes<CODE> pool;
+    pool.add(raw, true);
+    pool.get(R, mx, mn, sm);
     *reinterpret_cast<float4*>(&part[0][warp][4 * lane]) = make_float4(mx[0], mx[1], mx[2], mx[3]);
     *reinterpret_cast<float4*>(&part[1][warp][4 * lane]) = make_float4(mn[0], mn[1], mn[2], mn[3]);
     *reinterpret_cast<float4*>(&part[2][warp][4 * lane]) = make_float4(sm[0], sm[1], sm[2], sm[3]);
