@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 // g) of its eight: with the swizzle both operands' loads are then free of bank
 // conflicts.  The block's two scales enter as fp32 factors of S and O.
 // The current block comes from the bf16 tail on bf16 products (P as a sum of
-// two bf16 terms), rows past the length masked, while the ring first fills.
+// two bf16 terms, three for an fp32 output), rows past the length masked, while the ring first fills.
 //
 // Two ways to divide the work.  Lists (and dense attention without the
 // workspace for the other way): a cluster of CTAs a pair, which merge through
@@ -533,7 +533,8 @@ __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint
 }
 
 // One 16-key slice of the current block, from the bf16 tail: rows
-// row0 .. row0 + 15 of which those below `rows` count.
+// row0 .. row0 + 15 of which those below `rows` count.  P as TERMS bf16 terms.
+template <int TERMS>
 __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt, const __nv_bfloat16* vt,
                                             const __nv_bfloat16* q, bool head_ok, int row0, int rows, float scale) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -556,16 +557,19 @@ __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt
   sc[2] = in1 ? sc[2] * scale : -INFINITY;
   sc[3] = in1 ? sc[3] * scale : -INFINITY;
   raise_max(st, sc);
-  float p[4], lo[4];
+  float p[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    p[e] = (e < 2 ? in0 : in1) ? exp2_approx(sc[e] - st.m[e & 1]) : 0.f;
-    lo[e] = p[e] - __bfloat162float(__float2bfloat16_rn(p[e]));
-  }
+  for (int e = 0; e < 4; ++e) p[e] = (e < 2 ? in0 : in1) ? exp2_approx(sc[e] - st.m[e & 1]) : 0.f;
   st.l[0] += p[0] + p[2];
   st.l[1] += p[1] + p[3];
-  const uint32_t b0 = transpose8x8(pack_bf16x2(p[0], p[1])), b1 = transpose8x8(pack_bf16x2(p[2], p[3]));
-  const uint32_t e0 = transpose8x8(pack_bf16x2(lo[0], lo[1])), e1 = transpose8x8(pack_bf16x2(lo[2], lo[3]));
+  uint32_t b[TERMS][2];
+#pragma unroll
+  for (int n = 0; n < TERMS; ++n) {
+    const uint32_t h0 = pack_bf16x2(p[0], p[1]), h1 = pack_bf16x2(p[2], p[3]);
+    b[n][0] = transpose8x8(h0);
+    b[n][1] = transpose8x8(h1);
+    p[0] -= bf16_lo(h0), p[1] -= bf16_hi(h0), p[2] -= bf16_lo(h1), p[3] -= bf16_hi(h1);
+  }
   uint32_t v[4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -581,8 +585,8 @@ __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt
     const uint32_t sel = (j & 1) ? 0x7632 : 0x5410;
     const uint32_t a0 = __byte_perm(v[0][j / 2], v[1][j / 2], sel), a1 = __byte_perm(v[0][4 + j / 2], v[1][4 + j / 2], sel);
     const uint32_t a2 = __byte_perm(v[2][j / 2], v[3][j / 2], sel), a3 = __byte_perm(v[2][4 + j / 2], v[3][4 + j / 2], sel);
-    mma_bf16_16816(st.acc[j], a0, a1, a2, a3, b0, b1);
-    mma_bf16_16816(st.acc[j], a0, a1, a2, a3, e0, e1);
+#pragma unroll
+    for (int n = 0; n < TERMS; ++n) mma_bf16_16816(st.acc[j], a0, a1, a2, a3, b[n][0], b[n][1]);
   }
 }
 
@@ -811,7 +815,7 @@ __global__ void __launch_bounds__(256, 2)
   const bool tail_turn = CHUNKS ? (ch.q == ch.chunks - 1 && grp == 0) : grp == (m - 1) % js;
   if (!bad && tail_turn && 16 * quarter < L - c * kBlock) {
     const size_t off = static_cast<size_t>(pair) * (kBlock * kDim);
-    attend_tail(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * quarter, L - c * kBlock, p.scale_log2);
+    attend_tail<F32OUT ? 3 : 2>(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * quarter, L - c * kBlock, p.scale_log2);
   }
 
   // ---- the stored blocks
