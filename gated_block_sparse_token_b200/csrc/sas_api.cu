@@ -1111,7 +1111,7 @@ sas_status sas_pool_keys_kv8(const sas_config* cfg, const sas_kv8* kv, const int
   p.gk16 = cfg->gate_keys_bf16;
   p.pooled_raw = pooled_raw;
   p.status = static_cast<uint32_t*>(ws);
-  if (num_blocks <= sas::kPoolFewBlocks)
+  if (sas::pool_few(static_cast<long long>(kv->batch) * cfg->num_kv_heads, num_blocks) && num_blocks <= 65535)
     return launch_result(
         sas::launch_pool_few_kv8(kv->code, p, kv->batch, reinterpret_cast<cudaStream_t>(stream)));
   CUtensorMap tmwk;

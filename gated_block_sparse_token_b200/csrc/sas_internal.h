@@ -490,8 +490,15 @@ cudaError_t launch_kv8_attend(int code, bool f32_out, Kv8AttendParams p, cudaStr
 // pooling over the 8-bit cache: p.kv.k holds the codes, p.k_scale the scales
 cudaError_t launch_pool_project_kv8(int code, const PoolParams& p, const CUtensorMap& tmwk, int batch,
                                     cudaStream_t stream);
-// the same with one CTA a block, for up to kPoolFewBlocks blocks a sequence
-constexpr int kPoolFewBlocks = 4;
+// The same with one CTA a block, where that is sooner done.  Fitted to both
+// kernels: a wave of 148 single-block CTAs takes 2.8 us (and a launch 1), a wave
+// of the 128-block CTAs 9.5 us and 0.14 a block (32 pairs x 1 / 8 / 16 / 32 blocks:
+// 3.7 / 6.6 / 12.1 / 21.0 us against 9.8 / 10.5 / 10.5 / 12.8).
+inline bool pool_few(long long pairs, long long blocks) {
+  const long long few_waves = (pairs * blocks + 147) / 148;
+  const long long waves = (pairs * ((blocks + 127) / 128) + 147) / 148;
+  return 100 + 280 * few_waves <= waves * (950 + 14 * std::min(blocks, 128ll));
+}
 cudaError_t launch_pool_few_kv8(int code, const PoolParams& p, int batch, cudaStream_t stream);
 
 // One-time per-process set-up of kernel attributes.

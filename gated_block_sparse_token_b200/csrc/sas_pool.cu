@@ -343,11 +343,8 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
     return r < 0 ? -2 : r;
   };
   // rows that may hold work: blocks max(b0, 0) .. min(b0 + 128, b_end, mg, L / 64) - 1
-  {
-    const int lo = max(b0, 0);
-    const int hi = min(min(b0 + kPpRows, b_end), min(p.mg, L >= 1 ? L / kBlock : 0));
-    if (lo >= hi) return;  // uniform over the CTA
-  }
+  const int hi = min(min(b0 + kPpRows, b_end), min(p.mg, L >= 1 ? L / kBlock : 0));
+  if (max(b0, 0) >= hi) return;  // uniform over the CTA
 
   if (tid == 0) {
     prefetch_tensormap(&tmwk);
@@ -377,7 +374,9 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
     // unconditional loads (tile 0 for a row that is not pooled): a load under a
     // condition would be waited for where the paths meet
     load_codes(r0, kb + max(row, 0ll) * kDim);
-    for (int i = warp; i < kPpRows; i += STEP) {  // warp-uniform
+    // rows past the last block stay unwritten: the product's rows are
+    // independent, and theirs are not read
+    for (int i = warp; i < hi - b0; i += STEP) {  // warp-uniform
       if (row == -2) err = true;
       const long long row_2n = i + 2 * STEP < kPpRows ? row_of(i + 2 * STEP) : -1;
       float mx[4] = {0.f, 0.f, 0.f, 0.f}, mn[4] = {0.f, 0.f, 0.f, 0.f}, sm[4] = {0.f, 0.f, 0.f, 0.f};

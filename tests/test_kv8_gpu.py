@@ -177,11 +177,12 @@ def test_read_back(code, paged, out):
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("paged", [False, True])
 @pytest.mark.parametrize("gk16", [0, 1])
-def test_pool_keys(code, paged, gk16):
+@pytest.mark.parametrize("hkv", [1, 12])           # one CTA a block, and 128 blocks a CTA
+def test_pool_keys(code, paged, gk16, hkv):
     from oracle import sas_oracle as O
     lens = [64, 63, 700, 64 * 140 + 5]
-    B, hkv, blocks = len(lens), 2, 142
-    cfg = sas.Config(4, hkv, gate_keys_bf16=gk16)
+    B, blocks = len(lens), 142
+    cfg = sas.Config(hkv, hkv, gate_keys_bf16=gk16)
     kv = K.make_cache(B, hkv, blocks, code, paged, lens, DEV, seed=11)
     ws = ws_for(cfg)
     g = torch.Generator().manual_seed(4)
@@ -194,7 +195,7 @@ def test_pool_keys(code, paged, gk16):
     for s, L in enumerate(lens):
         n = L // 64
         assert bool((gk[s, :, n:] == 3).all()) and bool((raw[s, :, n:] == 3).all())
-        for h in range(hkv):
+        for h in sorted({0, hkv - 1}):
             if n == 0:
                 continue
             want_raw, vals = [], []
@@ -211,23 +212,24 @@ def test_pool_keys(code, paged, gk16):
 
 
 @pytest.mark.parametrize("code", CODES)
-@pytest.mark.parametrize("step", [1, 3, 5])
+@pytest.mark.parametrize("step", [1, 7, 20])
 def test_pool_keys_incremental_agrees_with_all_at_once(code, step):
     """Few blocks and many take different kernels, whose fp32 sums run in different orders: 384 products each, so
     the two agree to the bar of the gate keys; the same call twice is bit-identical."""
-    lens = [64 * 9, 64 * 5 + 3]
-    kv = K.make_cache(2, 2, 10, code, True, lens, DEV, seed=12)
-    cfg = sas.Config(2, 2)
+    n = 60
+    lens = [64 * n, 64 * 37 + 3]
+    kv = K.make_cache(2, 8, n, code, True, lens, DEV, seed=12)
+    cfg = sas.Config(8, 8)
     ws = ws_for(cfg)
-    w_k = (torch.randn((2, 384, 128), generator=torch.Generator().manual_seed(4)) / 20).bfloat16().to(DEV)
+    w_k = (torch.randn((8, 384, 128), generator=torch.Generator().manual_seed(4)) / 20).bfloat16().to(DEV)
     gamma = torch.ones(128, device=DEV)
-    a, a2, b = (torch.zeros(2, 2, 10, 128, device=DEV) for _ in range(3))
-    ra, rb = (torch.zeros(2, 2, 10, 384, device=DEV) for _ in range(2))
+    a, a2, b = (torch.zeros(2, 8, n, 128, device=DEV) for _ in range(3))
+    ra, rb = (torch.zeros(2, 8, n, 384, device=DEV) for _ in range(2))
     sas.pool_keys_kv8(cfg, kv, w_k, gamma, a, ws, pooled_raw=ra)
     sas.pool_keys_kv8(cfg, kv, w_k, gamma, a2, ws)
-    for i in range(0, 10, step):
+    for i in range(0, n, step):
         sas.pool_keys_kv8(cfg, kv, w_k, gamma, b, ws, num_blocks=step, pooled_raw=rb,
-                          blk_begin=torch.tensor([i, 10 - step - i], dtype=torch.int32, device=DEV))
+                          blk_begin=torch.tensor([i, n - step - i], dtype=torch.int32, device=DEV))
     assert ok(ws) and torch.equal(a, a2)
     assert torch.equal(ra[0], rb[0]) and torch.equal(a == 0, b == 0)
     T.assert_close_rel(b.cpu().numpy(), a.cpu().numpy(), "incremental")
