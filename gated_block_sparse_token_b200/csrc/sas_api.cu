@@ -927,7 +927,7 @@ sas_status norm_rope_call(const sas_config* cfg, const sas_rows* dq_out, const s
     return SAS_ERR_WORKSPACE;
   if (batch == 0 || seq_len == 0) return SAS_OK;
   if (!aligned(positions, 4)) return SAS_ERR_INVALID_ARG;
-  if (static_cast<long long>(batch) * seq_len > (1LL << 30)) return SAS_ERR_UNSUPPORTED;
+  if (static_cast<long long>(batch) * seq_len > (1LL << 29)) return SAS_ERR_UNSUPPORTED;  // int32 token numbers
   const bool f32 = cfg->kv_dtype == SAS_DTYPE_F32;
   const int64_t elem = f32 ? 4 : 2;
   bool has_q = false, has_k = false;
@@ -1122,7 +1122,8 @@ sas_status sas_pool_keys_kv8(const sas_config* cfg, const sas_kv8* kv, const int
 
 size_t sas_sparse_decode_kv8_workspace_bytes(const sas_config* cfg, int32_t batch) {
   if (check_config(cfg) != SAS_OK || batch <= 0) return ws_header_bytes();
-  return ws_header_bytes() + sas::kv8_attend_scratch_bytes(batch * cfg->num_kv_heads, cfg->num_q_heads / cfg->num_kv_heads);
+  return ws_header_bytes() + sas::kv8_attend_scratch_bytes(static_cast<long long>(batch) * cfg->num_kv_heads,
+                                                           cfg->num_q_heads / cfg->num_kv_heads);
 }
 
 sas_status sas_sparse_decode_kv8(const sas_config* cfg, const void* q, const sas_kv8* kv, const int32_t* sel_idx,

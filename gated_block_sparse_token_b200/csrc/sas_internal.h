@@ -485,7 +485,7 @@ struct Kv8AttendPlan {
   int cluster, groups;
 };
 Kv8AttendPlan kv8_attend_plan(int pairs, int max_blocks);
-size_t kv8_attend_scratch_bytes(int pairs, int G);
+size_t kv8_attend_scratch_bytes(long long pairs, int G);
 cudaError_t launch_kv8_attend(int code, bool f32_out, Kv8AttendParams p, cudaStream_t stream);
 // pooling over the 8-bit cache: p.kv.k holds the codes, p.k_scale the scales
 cudaError_t launch_pool_project_kv8(int code, const PoolParams& p, const CUtensorMap& tmwk, int batch,

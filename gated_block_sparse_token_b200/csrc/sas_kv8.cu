@@ -1076,9 +1076,9 @@ Kv8AttendPlan kv8_attend_plan(int pairs, int max_blocks) {
 
 // The grid holds target + pairs chunks at most.  Up to 74 pairs they all fit
 // the GPU at once (2 x 148 CTAs); more pairs have no use for a single wave.
-static int chunk_target(int pairs) { return pairs <= 74 ? 2 * 148 - pairs : 4 * 148; }
+static long long chunk_target(long long pairs) { return pairs <= 74 ? 2 * 148 - pairs : 4 * 148; }
 
-size_t kv8_attend_scratch_bytes(int pairs, int G) {
+size_t kv8_attend_scratch_bytes(long long pairs, int G) {
   return static_cast<size_t>(chunk_target(pairs) + pairs) * (static_cast<size_t>(G) * kDim + 2 * kMaxGroup + 4) * 4;
 }
 
@@ -1088,7 +1088,7 @@ cudaError_t launch_kv8_attend(int code, bool f32_out, Kv8AttendParams p, cudaStr
   // holds their partial sums
   if (p.sel_idx == nullptr && p.ws_part != nullptr && p.batch <= kKaMaxChunkBatch && p.kv.blocks > 4 * kKaChunkMin) {
     constexpr size_t smem = kKaMaxWarps * std::max(kKaStages * kKaSlot, kKaPart * 4);
-    p.target = chunk_target(pairs);
+    p.target = static_cast<int>(chunk_target(pairs));
     const dim3 grid(static_cast<unsigned>(p.target + pairs)), cgrid(static_cast<unsigned>(pairs), static_cast<unsigned>(p.G));
     cudaError_t e;
     if (code == kCodeE4m3)

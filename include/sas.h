@@ -474,7 +474,7 @@ typedef struct {
  *              cfg->rope_base is the gate's
  *   q, k       inputs [B][Hq][T] and [B][Hkv][T] rows; either may be NULL (and
  *              its output with it): the other alone is computed
- *   positions  int32 [B][T] on the device, or NULL: t.  A row whose position
+ *   positions  int32 [B][T] on the device, or NULL: t (B * T at most 2^29).  A row whose position
  *              is negative (padding) is skipped: its output stays as it was
  *   q_out, k_out  may be the inputs themselves (same data and strides); any
  *              other overlap, and rows of one output that overlap, are the
@@ -498,6 +498,7 @@ SAS_API size_t sas_qk_norm_rope_workspace_bytes(void);
  * with a negative position are skipped and contribute nothing.  Queries or
  * keys may be left out as in the forward (all of their pointers NULL).
  *   ws  at least sas_qk_norm_rope_workspace_bytes() bytes, 16-byte aligned
+ *       (partial sums: calls that may overlap on the GPU need one each)
  */
 SAS_API sas_status sas_qk_norm_rope_backward(const sas_config* cfg, const sas_rows* dq_out,
                                              const sas_rows* dk_out, const sas_rows* q,
