@@ -104,19 +104,18 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const __grid_constan
     const uint32_t abits = finite ? max(m << 16, kMinAmaxBits) : 0x3f800000u;
     const float a = __uint_as_float(abits);
     constexpr float qmax = CODE == kCodeE4m3 ? kQmaxE4m3 : kQmaxInt8;
-    // Quotient x qmax / a to within its last bit, and exact where it is
-    // representable (so also where it lies half-way between two codes): a and
-    // x are first scaled by 2^(1-e), e the exponent of a, which keeps every
-    // term in range; then one correction step with the exact remainder.  A
-    // quotient of bf16 values that is no half-way point is at least 2^-16 of
-    // its value away from one, so the code is that of the exact quotient.
+    // The rounded quotient x qmax / a, exact where it is representable (so also
+    // where it lies half-way between two codes).  qmax / a is taken as Rh + Rl, Rh
+    // its leading 16 bits: x Rh is exact (8 bits by 16), and x (Rh + Rl) within
+    // 2^-38 of the quotient before its one rounding.  A quotient of bf16 values
+    // that is no half-way point is at least 2^-16 of its value away from one, so
+    // the code is that of the exact quotient.  a is first scaled to [2, 4) and
+    // the factors by the same power of two, which keeps every term in range.
     const float pw = __uint_as_float(((255u - (abits >> 23)) << 23));
-    const float an = a * pw, inv = 1.f / an;
-    const float R = qmax / an * pw, T = qmax * pw;
-    const auto quot = [&](float v) {
-      const float q = v * R;
-      return fmaf(fmaf(-q, an, v * T), inv, q);
-    };
+    const float an = a * pw;
+    const float rh = __uint_as_float(__float_as_uint(qmax / an) & 0xffffff00u);
+    const float Rh = rh * pw, Rl = fmaf(-rh, an, qmax) / an * pw;
+    const auto quot = [&](float v) { return fmaf(v, Rl, v * Rh); };
     uint2 code[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -384,15 +383,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {

@@ -249,7 +249,10 @@ void fill_rope_table(RopeTable& t, float base) {
 // SRC: the cache's elements, bf16 or (an 8-bit cache) codes under one scale a
 // block.  Codes and their mean are pooled in units of the scale -- exact in
 // bf16, the mean as hi + lo -- and the epilogue multiplies u by the block's
-// scale, so the 8-bit form reads half the bytes and rounds nothing more.
+// scale, so the 8-bit form reads half the bytes and rounds nothing more.  Its
+// codes come through a cp.async ring in the space of W_k, which is fetched (from
+// L2) once the pooling is done: with 227 KiB of shared memory taken, the L1 that
+// ordinary loads return through holds too little in flight (39.4 us).
 constexpr int kPpRows = 128;          // blocks per CTA (the MMA's M)
 constexpr int kPpThreads = 256;
 constexpr int kPpA = kPpRows * 512 * 2;           // A operand bytes (8 chunks of 16 KiB)
@@ -346,15 +349,18 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
   const int hi = min(min(b0 + kPpRows, b_end), min(p.mg, L >= 1 ? L / kBlock : 0));
   if (max(b0, 0) >= hi) return;  // uniform over the CTA
 
+  const auto fetch_wk = [&]() {  // one thread
+    mbar_arrive_expect_tx(&bars[0], kPpB);
+    for (int c = 0; c < 2; ++c)
+      for (int r = 0; r < kPool / 64; ++r)
+        tma_load_2d(sB + c * (kPool * 128) + r * 8192, &tmwk, 64 * c, h * kPool + 64 * r, &bars[0]);
+  };
   if (tid == 0) {
     prefetch_tensormap(&tmwk);
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
     fence_mbar_init();
-    mbar_arrive_expect_tx(&bars[0], kPpB);
-    for (int c = 0; c < 2; ++c)
-      for (int r = 0; r < kPool / 64; ++r)
-        tma_load_2d(sB + c * (kPool * 128) + r * 8192, &tmwk, 64 * c, h * kPool + 64 * r, &bars[0]);
+    if (SRC == kSrcBf16) fetch_wk();
   }
   if (warp == 0) {
     tmem_alloc(tmem_slot, 128);
@@ -364,27 +370,45 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
   // ---- pooling into the A operand
   if constexpr (SRC != kSrcBf16) {
     bool err = false;
-    // a warp's blocks i, i + 16, ..: each in two halves of 32 rows, the next
-    // half's loads in flight while one is worked on, the next block's cache row
-    // known a block ahead
-    constexpr int STEP = pp_threads(SRC) / 32;
-    uint32_t r0[kBlock / 2], r1[kBlock / 2];
-    const uint8_t* kb = static_cast<const uint8_t*>(p.kv.k) + 4 * lane;
+    // a warp's blocks i, i + 16, ..: each in quarters of 16 rows through the warp's
+    // ring of three; the next block's cache row known a block ahead
+    constexpr int STEP = pp_threads(SRC) / 32, Q = 16, SLOTS = 3, SLOT = Q * kDim;
+    static_assert(STEP * SLOTS * SLOT <= kPpB, "the rings fit W_k's space");
+    const uint32_t ring = smem_u32(sB) + warp * (SLOTS * SLOT);
+    const uint8_t* kb = static_cast<const uint8_t*>(p.kv.k);
     long long row = row_of(warp), row_n = row_of(warp + STEP);
-    // unconditional loads (tile 0 for a row that is not pooled): a load under a
-    // condition would be waited for where the paths meet
-    load_codes(r0, kb + max(row, 0ll) * kDim);
-    // rows past the last block stay unwritten: the product's rows are
-    // independent, and theirs are not read
-    for (int i = warp; i < hi - b0; i += STEP) {  // warp-uniform
+    const int n_rows = hi - b0;  // rows past the last block stay unwritten: the product's
+                                 // rows are independent, and theirs are not read
+    const auto issue = [&](uint32_t slot, long long r, int k) {  // quarter k of the block at row r
+      if (r >= 0) {
+        const uint8_t* src = kb + (r + Q * k) * kDim + 16 * lane;
+#pragma unroll
+        for (int i = 0; i < SLOT / 512; ++i) cp_async16(slot + 512 * i + 16 * lane, src + 512 * i);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < SLOTS; ++k) issue(ring + k * SLOT, warp < n_rows ? row : -1, k);
+    uint32_t slot = ring;
+    for (int i = warp; i < n_rows; i += STEP) {  // warp-uniform
       if (row == -2) err = true;
       const long long row_2n = i + 2 * STEP < kPpRows ? row_of(i + 2 * STEP) : -1;
+      const long long next = i + STEP < n_rows ? row_n : -1;
       float mx[4] = {0.f, 0.f, 0.f, 0.f}, mn[4] = {0.f, 0.f, 0.f, 0.f}, sm[4] = {0.f, 0.f, 0.f, 0.f};
       PooledCodes<SRC> pool;
-      load_codes(r1, kb + (max(row, 0ll) + kBlock / 2) * kDim);
-      pool.add(r0, true);
-      load_codes(r0, kb + max(row_n, 0ll) * kDim);
-      pool.add(r1, false);
+#pragma unroll
+      for (int k = 0; k < kBlock / Q; ++k) {
+        cp_async_wait<SLOTS - 1>();
+        __syncwarp();
+        uint32_t r[Q];
+#pragma unroll
+        for (int v = 0; v < Q; ++v)
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[v]) : "r"(slot + v * kDim + 4 * lane) : "memory");
+        __syncwarp();  // the slot is read: refill it
+        issue(slot, k + SLOTS < kBlock / Q ? row : next, (k + SLOTS) % (kBlock / Q));
+        pool.add(r, k == 0);
+        slot = slot + SLOT == ring + SLOTS * SLOT ? ring : slot + SLOT;
+      }
       if (row >= 0) pool.get(kBlock, mx, mn, sm);
       uint32_t pk[4][2];
 #pragma unroll
@@ -415,6 +439,7 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
       row = row_n;
       row_n = row_2n;
     }
+    cp_async_wait<0>();
     if (err && lane == 0) raise_status(p.status, kStatusBounds);
   } else {
     constexpr int TPR = 16;             // lanes per K row (16-byte loads)
@@ -505,6 +530,7 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
 
   // ---- u = A @ B on the tensor cores
   if (tid == 0) {
+    if (SRC != kSrcBf16) fetch_wk();  // every thread has fenced its use of the ring
     const bool okb = mbar_wait(&bars[0], 0, p.status);
     tc_fence_after_sync();
     if (okb) {
