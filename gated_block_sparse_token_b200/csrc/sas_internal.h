@@ -362,6 +362,29 @@ cudaError_t launch_gate_backward(const GateBwdParams& p, const CUtensorMap& tmk,
 cudaError_t launch_prefill_gate_backward(const PrefillBwdParams& p, const CUtensorMap& tmq, const CUtensorMap& tmk,
                                          const CUtensorMap& tmv, cudaStream_t stream);
 
+// ---------------------------------------------------------------- launches
+// A launch with programmatic stream serialization, in clusters of `cluster`
+// CTAs (0: none).
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                       const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  a[1].val.clusterDim.y = 1;
+  a[1].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------- norms with rotation
 // Rows of 128 elements of a [sequence][head][token] tensor with any strides
 // (in elements).

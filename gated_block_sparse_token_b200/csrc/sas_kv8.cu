@@ -996,30 +996,6 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------- launches
-namespace {
-
-template <typename... Args>
-cudaError_t launch(void (*k)(Args...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
-                   const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute a[2];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  a[1].id = cudaLaunchAttributeClusterDimension;
-  a[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  a[1].val.clusterDim.y = 1;
-  a[1].val.clusterDim.z = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
-}
-
-}  // namespace
-
 // CTAs of one (sequence, head) that walk `blocks` blocks: four waves of three an
 // SM over all pairs (a ragged batch levels out), or about four blocks a CTA if
 // that makes more, at most one a block.  Read-back of 32 pairs x 513 blocks with
@@ -1035,8 +1011,8 @@ cudaError_t launch_kv8_append(int code, const Kv8AppendParams& p, int batch, cud
   const long long blocks = (static_cast<long long>(p.max_new) + kBlock - 1) / kBlock;
   const dim3 grid(walkers(blocks, static_cast<long long>(batch) * p.kv.hkv), static_cast<unsigned>(p.kv.hkv),
                   static_cast<unsigned>(batch));
-  return code == kCodeE4m3 ? launch(kv8_append_kernel<kCodeE4m3>, grid, 256, 0, 0, stream, p)
-                           : launch(kv8_append_kernel<kCodeInt8>, grid, 256, 0, 0, stream, p);
+  return code == kCodeE4m3 ? launch_pdl(kv8_append_kernel<kCodeE4m3>, grid, 256, 0, stream, 0, p)
+                           : launch_pdl(kv8_append_kernel<kCodeInt8>, grid, 256, 0, stream, 0, p);
 }
 
 cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int batch, cudaStream_t stream) {
@@ -1044,10 +1020,10 @@ cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int 
   const dim3 grid(walkers(blocks, static_cast<long long>(batch) * p.kv.hkv), static_cast<unsigned>(p.kv.hkv),
                   static_cast<unsigned>(batch));
   if (code == kCodeE4m3)
-    return f32_out ? launch(kv8_read_kernel<kCodeE4m3, float>, grid, 256, 0, 0, stream, p)
-                   : launch(kv8_read_kernel<kCodeE4m3, __nv_bfloat16>, grid, 256, 0, 0, stream, p);
-  return f32_out ? launch(kv8_read_kernel<kCodeInt8, float>, grid, 256, 0, 0, stream, p)
-                 : launch(kv8_read_kernel<kCodeInt8, __nv_bfloat16>, grid, 256, 0, 0, stream, p);
+    return f32_out ? launch_pdl(kv8_read_kernel<kCodeE4m3, float>, grid, 256, 0, stream, 0, p)
+                   : launch_pdl(kv8_read_kernel<kCodeE4m3, __nv_bfloat16>, grid, 256, 0, stream, 0, p);
+  return f32_out ? launch_pdl(kv8_read_kernel<kCodeInt8, float>, grid, 256, 0, stream, 0, p)
+                 : launch_pdl(kv8_read_kernel<kCodeInt8, __nv_bfloat16>, grid, 256, 0, stream, 0, p);
 }
 
 // Two groups a CTA (two such CTAs an SM), and as many CTAs a cluster as keep
@@ -1082,24 +1058,24 @@ cudaError_t launch_kv8_attend(int code, bool f32_out, Kv8AttendParams p, cudaStr
     const dim3 grid(static_cast<unsigned>(p.target + pairs)), cgrid(static_cast<unsigned>(pairs), static_cast<unsigned>(p.G));
     cudaError_t e;
     if (code == kCodeE4m3)
-      e = f32_out ? launch(kv8_attend_kernel<kCodeE4m3, true, true>, grid, 256, smem, 0, stream, p)
-                  : launch(kv8_attend_kernel<kCodeE4m3, false, true>, grid, 256, smem, 0, stream, p);
+      e = f32_out ? launch_pdl(kv8_attend_kernel<kCodeE4m3, true, true>, grid, 256, smem, stream, 0, p)
+                  : launch_pdl(kv8_attend_kernel<kCodeE4m3, false, true>, grid, 256, smem, stream, 0, p);
     else
-      e = f32_out ? launch(kv8_attend_kernel<kCodeInt8, true, true>, grid, 256, smem, 0, stream, p)
-                  : launch(kv8_attend_kernel<kCodeInt8, false, true>, grid, 256, smem, 0, stream, p);
+      e = f32_out ? launch_pdl(kv8_attend_kernel<kCodeInt8, true, true>, grid, 256, smem, stream, 0, p)
+                  : launch_pdl(kv8_attend_kernel<kCodeInt8, false, true>, grid, 256, smem, stream, 0, p);
     if (e != cudaSuccess) return e;
-    return f32_out ? launch(kv8_combine_kernel<true>, cgrid, 256, 0, 0, stream, p)
-                   : launch(kv8_combine_kernel<false>, cgrid, 256, 0, 0, stream, p);
+    return f32_out ? launch_pdl(kv8_combine_kernel<true>, cgrid, 256, 0, stream, 0, p)
+                   : launch_pdl(kv8_combine_kernel<false>, cgrid, 256, 0, stream, 0, p);
   }
   const Kv8AttendPlan a = kv8_attend_plan(pairs, p.sel_idx != nullptr ? p.max_sel : p.kv.blocks);
   const dim3 grid(static_cast<unsigned>(a.cluster), static_cast<unsigned>(pairs));
   const int T = 128 * a.groups;
   const size_t smem = static_cast<size_t>(4 * a.groups) * std::max(kKaStages * kKaSlot, kKaPart * 4);
   if (code == kCodeE4m3)
-    return f32_out ? launch(kv8_attend_kernel<kCodeE4m3, true, false>, grid, T, smem, a.cluster, stream, p)
-                   : launch(kv8_attend_kernel<kCodeE4m3, false, false>, grid, T, smem, a.cluster, stream, p);
-  return f32_out ? launch(kv8_attend_kernel<kCodeInt8, true, false>, grid, T, smem, a.cluster, stream, p)
-                 : launch(kv8_attend_kernel<kCodeInt8, false, false>, grid, T, smem, a.cluster, stream, p);
+    return f32_out ? launch_pdl(kv8_attend_kernel<kCodeE4m3, true, false>, grid, T, smem, stream, a.cluster, p)
+                   : launch_pdl(kv8_attend_kernel<kCodeE4m3, false, false>, grid, T, smem, stream, a.cluster, p);
+  return f32_out ? launch_pdl(kv8_attend_kernel<kCodeInt8, true, false>, grid, T, smem, stream, a.cluster, p)
+                 : launch_pdl(kv8_attend_kernel<kCodeInt8, false, false>, grid, T, smem, stream, a.cluster, p);
 }
 
 cudaError_t prepare_kv8_kernels() {

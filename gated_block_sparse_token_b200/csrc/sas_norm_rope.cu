@@ -217,24 +217,6 @@ __global__ void __launch_bounds__(1024) norm_rope_gain_kernel(const float* part,
   }
 }
 
-namespace {
-
-template <typename... Args>
-cudaError_t launch_pdl(void (*k)(Args...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.stream = stream;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
-}
-
-}  // namespace
-
 cudaError_t launch_norm_rope(bool f32, bool back, NormRopeParams p, float* dgamma_q, float* dgamma_k,
                              cudaStream_t stream) {
   const NormRopeGrid g = norm_rope_grid(p.batch, p.tokens, p.hq, p.hkv, back);
@@ -243,14 +225,13 @@ cudaError_t launch_norm_rope(bool f32, bool back, NormRopeParams p, float* dgamm
   const dim3 grid(static_cast<unsigned>(g.x), static_cast<unsigned>(g.q_chunks + g.k_chunks));
   cudaError_t e;
   if (!back) {
-    return f32 ? launch_pdl(norm_rope_kernel<float, false>, grid, kNrThreads, stream, p)
-               : launch_pdl(norm_rope_kernel<__nv_bfloat16, false>, grid, kNrThreads, stream, p);
+    return f32 ? launch_pdl(norm_rope_kernel<float, false>, grid, kNrThreads, 0, stream, 0, p)
+               : launch_pdl(norm_rope_kernel<__nv_bfloat16, false>, grid, kNrThreads, 0, stream, 0, p);
   }
-  e = f32 ? launch_pdl(norm_rope_kernel<float, true>, grid, kNrThreads, stream, p)
-          : launch_pdl(norm_rope_kernel<__nv_bfloat16, true>, grid, kNrThreads, stream, p);
+  e = f32 ? launch_pdl(norm_rope_kernel<float, true>, grid, kNrThreads, 0, stream, 0, p)
+          : launch_pdl(norm_rope_kernel<__nv_bfloat16, true>, grid, kNrThreads, 0, stream, 0, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_rope_gain_kernel, dim3(kDim / 32, 2), 1024, stream,
-                    static_cast<const float*>(p.ws_part), g.q_chunks * g.x, g.k_chunks * g.x, dgamma_q, dgamma_k);
+  return launch_pdl(norm_rope_gain_kernel, dim3(kDim / 32, 2), 1024, 0, stream, 0, p.ws_part, g.q_chunks * g.x, g.k_chunks * g.x, dgamma_q, dgamma_k);
 }
 
 }  // namespace sas

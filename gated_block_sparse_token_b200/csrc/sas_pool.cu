@@ -317,13 +317,17 @@ __device__ __forceinline__ void load_codes(uint32_t (&raw)[ROWS], const uint8_t*
 }
 
 // Threads of the kernel for a source: codes are pooled by sixteen warps (the
-// loop over a block's words is bound by instruction issue, half the bytes a
-// word more than for bf16), of which the first eight run the epilogue.
+// loop over a block's words is bound by instruction issue, twice the values a
+// word of bf16).
 __host__ __device__ constexpr int pp_threads(int src) { return src == kSrcBf16 ? kPpThreads : 2 * kPpThreads; }
 
 template <int SRC>
 __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const __grid_constant__ PoolParams p,
                                                                      const __grid_constant__ CUtensorMap tmwk) {
+  if constexpr (SRC != kSrcBf16) {  // launched with programmatic stream serialization
+    griddep_launch_dependents();
+    griddep_wait();
+  }
   const int s = blockIdx.z;
   const int h = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -551,39 +555,44 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
 
   // ---- epilogue: RMSNorm, gain, RoPE at the block index, store
   {
-    const int q4 = warp & 3, hf = warp >> 2;  // lane quarter; half of the rotate-half pairs
+    // lane quarter; part of the rotate-half pairs, W of them
+    constexpr int PARTS = pp_threads(SRC) / 128, W = 64 / PARTS;
+    const int q4 = warp & 3, hf = warp >> 2;
     const int i = 32 * q4 + lane;             // tile row = block b0 + i
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
-    const bool mine = SRC == kSrcBf16 || hf < 2;  // warp-uniform
-    float lo[32], hi[32];
-    if (mine) {
-      tmem_ld32(tl + 32 * hf, lo);       // columns 32 hf .. 32 hf + 31
-      tmem_ld32(tl + 64 + 32 * hf, hi);  // their rotate-half partners
-      tmem_wait_ld();
+    float* sq = SRC == kSrcBf16 ? ssq : reinterpret_cast<float*>(sA);  // four parts: over A, which is used
+    float lo[W], hi[W];
+    if constexpr (W == 32) {
+      tmem_ld32(tl + W * hf, lo);       // columns W hf .. W hf + W - 1
+      tmem_ld32(tl + 64 + W * hf, hi);  // their rotate-half partners
+    } else {
+      tmem_ld16(tl + W * hf, lo);
+      tmem_ld16(tl + 64 + W * hf, hi);
     }
-    const long long row = mine ? row_of(i) : -1;
+    tmem_wait_ld();
+    const long long row = row_of(i);
     if constexpr (SRC != kSrcBf16) {
       const float sc = row >= 0 ? p.k_scale[row / kBlock] : 0.f;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < W; ++k) {
         lo[k] *= sc;
         hi[k] *= sc;
       }
     }
-    if (mine) {
-      float ss = 0.f;
+    float ss = 0.f;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) ss = fmaf(lo[k], lo[k], fmaf(hi[k], hi[k], ss));
-      ssq[hf * kPpRows + i] = ss;
-    }
+    for (int k = 0; k < W; ++k) ss = fmaf(lo[k], lo[k], fmaf(hi[k], hi[k], ss));
+    sq[hf * kPpRows + i] = ss;
     __syncthreads();
     if (row >= 0 && okm) {
       const int b = b0 + i;
-      const float inv = 1.f / sqrtf((ssq[i] + ssq[kPpRows + i]) / kDim + p.eps);
+      float tot = sq[i] + sq[kPpRows + i];
+      if constexpr (PARTS == 4) tot += sq[2 * kPpRows + i] + sq[3 * kPpRows + i];
+      const float inv = 1.f / sqrtf(tot / kDim + p.eps);
       const size_t gi = ((static_cast<size_t>(s) * p.hkv + h) * p.mg + b) * kDim;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int d = 32 * hf + k;
+      for (int k = 0; k < W; ++k) {
+        const int d = W * hf + k;
         const float x0 = lo[k] * inv * p.gamma_k[d];
         const float x1 = hi[k] * inv * p.gamma_k[d + 64];
         float cs, sn;
@@ -594,20 +603,20 @@ __global__ void __launch_bounds__(pp_threads(SRC), 1) pool_project_kernel(const 
       if (p.gk16) {
         __nv_bfloat16* g = static_cast<__nv_bfloat16*>(p.gate_keys) + gi;
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          *reinterpret_cast<uint4*>(g + 32 * hf + k) =
+        for (int k = 0; k < W; k += 8) {
+          *reinterpret_cast<uint4*>(g + W * hf + k) =
               make_uint4(pack_bf16x2(lo[k], lo[k + 1]), pack_bf16x2(lo[k + 2], lo[k + 3]),
                          pack_bf16x2(lo[k + 4], lo[k + 5]), pack_bf16x2(lo[k + 6], lo[k + 7]));
-          *reinterpret_cast<uint4*>(g + 64 + 32 * hf + k) =
+          *reinterpret_cast<uint4*>(g + 64 + W * hf + k) =
               make_uint4(pack_bf16x2(hi[k], hi[k + 1]), pack_bf16x2(hi[k + 2], hi[k + 3]),
                          pack_bf16x2(hi[k + 4], hi[k + 5]), pack_bf16x2(hi[k + 6], hi[k + 7]));
         }
       } else {
         float* g = static_cast<float*>(p.gate_keys) + gi;
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          *reinterpret_cast<float4*>(g + 32 * hf + k) = make_float4(lo[k], lo[k + 1], lo[k + 2], lo[k + 3]);
-          *reinterpret_cast<float4*>(g + 64 + 32 * hf + k) = make_float4(hi[k], hi[k + 1], hi[k + 2], hi[k + 3]);
+        for (int k = 0; k < W; k += 4) {
+          *reinterpret_cast<float4*>(g + W * hf + k) = make_float4(lo[k], lo[k + 1], lo[k + 2], lo[k + 3]);
+          *reinterpret_cast<float4*>(g + 64 + W * hf + k) = make_float4(hi[k], hi[k + 1], hi[k + 2], hi[k + 3]);
         }
       }
     }
@@ -629,11 +638,8 @@ cudaError_t launch_pool_project_kv8(int code, const PoolParams& p, const CUtenso
                                     cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((p.num_blocks + kPpRows - 1) / kPpRows), static_cast<unsigned>(p.hkv),
                   static_cast<unsigned>(batch));
-  if (code == kCodeE4m3)
-    pool_project_kernel<kSrcE4m3><<<grid, pp_threads(kSrcE4m3), kPpSmem, stream>>>(p, tmwk);
-  else
-    pool_project_kernel<kSrcInt8><<<grid, pp_threads(kSrcInt8), kPpSmem, stream>>>(p, tmwk);
-  return cudaGetLastError();
+  return code == kCodeE4m3 ? launch_pdl(pool_project_kernel<kSrcE4m3>, grid, pp_threads(kSrcE4m3), kPpSmem, stream, 0, p, tmwk)
+                           : launch_pdl(pool_project_kernel<kSrcInt8>, grid, pp_threads(kSrcInt8), kPpSmem, stream, 0, p, tmwk);
 }
 
 // ---------------------------------------------------------------- few blocks
@@ -735,17 +741,9 @@ __global__ void __launch_bounds__(kPfThreads) pool_few_kernel(const __grid_const
 }
 
 cudaError_t launch_pool_few_kv8(int code, const PoolParams& p, int batch, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.num_blocks), static_cast<unsigned>(p.hkv), static_cast<unsigned>(batch));
-  cfg.blockDim = dim3(kPfThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
-  return code == kCodeE4m3 ? cudaLaunchKernelEx(&cfg, pool_few_kernel<kCodeE4m3>, p)
-                           : cudaLaunchKernelEx(&cfg, pool_few_kernel<kCodeInt8>, p);
+  const dim3 grid(static_cast<unsigned>(p.num_blocks), static_cast<unsigned>(p.hkv), static_cast<unsigned>(batch));
+  return code == kCodeE4m3 ? launch_pdl(pool_few_kernel<kCodeE4m3>, grid, kPfThreads, 0, stream, 0, p)
+                           : launch_pdl(pool_few_kernel<kCodeInt8>, grid, kPfThreads, 0, stream, 0, p);
 }
 
 cudaError_t prepare_pool_project_kernel() {
