@@ -502,12 +502,6 @@ struct Kv8AttendParams {
 
 cudaError_t launch_kv8_append(int code, const Kv8AppendParams& p, int batch, cudaStream_t stream);
 cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int batch, cudaStream_t stream);
-// How the attention splits: CTAs of a cluster (one cluster a pair), groups of
-// four warps of a CTA.
-struct Kv8AttendPlan {
-  int cluster, groups;
-};
-Kv8AttendPlan kv8_attend_plan(int pairs, int max_blocks);
 size_t kv8_attend_scratch_bytes(long long pairs, int G);
 cudaError_t launch_kv8_attend(int code, bool f32_out, Kv8AttendParams p, cudaStream_t stream);
 // pooling over the 8-bit cache: p.kv.k holds the codes, p.k_scale the scales

@@ -268,53 +268,59 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 // blocks (or of every block), one cluster of CTAs per (sequence, KV head).
 //
 // Bound by memory: 16 KiB of codes a block.  A group of four warps takes whole
-// blocks, 16 keys a warp; a CTA holds one group or two.  Every warp streams
-// its own 4 KiB slices through its own ring of kKaStages slots (cp.async, 16
-// bytes a lane): the loop has no barrier and no producer, and tens of KiB are in
-// flight on every SM whatever the register use.  (Loads into registers, one
-// slice ahead, left too little in flight: 84 us for 32 ragged sequences of
-// 4,096 listed tokens against 59; a ring fed by 2-D TMA from a lane of one of
-// the consuming warps cost that warp the issue of two copies a block.)
+// blocks, 16 keys a warp; a CTA holds two groups.  Every warp streams its own
+// 4 KiB slices through its own ring of kKaStages slots (cp.async, 16 bytes a
+// lane): the loop has no barrier and no producer, and 192 KiB are in flight on
+// an SM whatever the register use.  (Loads into registers, one slice ahead, left
+// too little in flight: 84 us for 256 pairs x 64 blocks; a ring fed by 2-D TMA
+// from a lane of one of the consuming warps, which spends that warp's time on
+// two copies a block: 59; this one 53.)
 //   S^T = K q^T  the 16 keys are the rows, the (up to 8) heads of the group the
 //                columns.  int8: m16n8k32 on the codes as they are stored, the
 //                query as the signed 8-bit digits of a fixed-point number per
-//                head (two digits, 2^-15 of the head's largest value, for a bf16
-//                output, three, 2^-23, for fp32); its sums are exact.  e4m3:
-//                m16n8k16 f16, the codes converted (exact), the query scaled by
-//                a power of two per head into f16's range (its bf16 values stay
-//                exact down to 2^-24 of the largest).  (The e4m3 form of
+//                head: two digits, 2^-16 of the head's largest value (its bf16
+//                values carry 2^-8 of their own), for a bf16 output, three, 2^-23,
+//                for fp32; its sums are exact.  e4m3: m16n8k16 f16, the codes
+//                converted (exact), the query scaled by a power of two per head
+//                into f16's range (its bf16 values stay exact down to 2^-15 of the
+//                largest, and off by 2^-25 of it below).  (The e4m3 form of
 //                m16n8k32 with the query as two e4m3 terms ran slower than the
 //                conversions it saves: 144 us against 114 for 2 x 128k tokens.)
 //   softmax      per head over the columns, fp32, base 2; the running maximum
 //                moves only when it grows by more than 2^8 (any factor common
 //                to p and its sum cancels), so most blocks need one vote and
 //                no shuffles;
-//   O^T += V^T P^T  m16n8k16 f16 (codes are exact in f16), the P fragment transposed in place by movmatrix.  P is
-//                rounded to f16 (2^-12 relative, before a bf16 output); for an
-//                fp32 output a second product carries the remainder.  The sum
-//                runs over the unrounded p.
+//   O^T += V^T P^T  m16n8k16 f16 (codes are exact in f16), the P fragment
+//                transposed in place by movmatrix.  P is rounded to f16 (2^-11
+//                relative, before a bf16 output); for an fp32 output a second
+//                product carries the remainder.  The sum of P runs over the
+//                unrounded values.
 // Both products take their k index from whatever order makes a lane's 16-byte
 // shared load its fragment: dims 16t .. 16t+15 and 64 + those for K, dims 16g ..
 // of four keys for V.  Key g of a fragment is row 2(g/2) + g/4 (xor 4 for odd
 // g) of its eight: with the swizzle both operands' loads are then free of bank
 // conflicts.  The block's two scales enter as fp32 factors of S and O.
 // The current block comes from the bf16 tail on bf16 products (P as a sum of
-// two bf16 terms, three for an fp32 output), rows past the length masked, while the ring first fills.
+// two bf16 terms, three for an fp32 output), rows past the length masked, while
+// the ring first fills.
 //
 // Two ways to divide the work.  Lists (and dense attention without the
 // workspace for the other way): a cluster of CTAs a pair, which merge through
 // distributed shared memory.  Dense attention (CHUNKS): every sequence in chunks
 // of equal length, one CTA a (chunk, head), so that few or ragged long
-// sequences fill the SMs; a second kernel merges the chunks' partial sums
-// (16 pairs x 2,000 blocks: clusters of 8 114-121 us, of 16, which not every
+// sequences fill the SMs; a second kernel merges the chunks' partial sums (16
+// pairs x 2,000 blocks: 92-101 us; clusters of 8 114-121, of 16, which not every
 // GPC holds twice, 105-118).
-constexpr int kKaStages = 3;                       // ring slots of a warp
-constexpr int kKaSlot = 2 * 16 * kDim;             // 16 rows of K, then of V
-constexpr int kKaHeadPair = 2 * kDim + 4;  // floats between head pairs of a partial (bank spread)
+// Measured: 64 pairs x 32 blocks 11.6 us (2.9 TB/s; the launch, the chain of
+// length, list, table and first tile, and the merge are half of it), 256 pairs x
+// 64 blocks 53 us (5.1 TB/s), 128 pairs x 500 blocks dense 172 us (6.0 TB/s).
+constexpr int kKaStages = 3;                // ring slots of a warp
+constexpr int kKaSlot = 2 * 16 * kDim;      // 16 rows of K, then of V
+constexpr int kKaHeadPair = 2 * kDim + 4;   // floats between head pairs of a partial (bank spread)
 constexpr int kKaPart = (kMaxGroup / 2) * kKaHeadPair;
-constexpr int kKaMaxWarps = 8;
-constexpr int kKaMaxChunkBatch = 1024;  // sequences that the chunked way handles
-constexpr int kKaChunkMin = 16;         // blocks of a chunk, at least
+constexpr int kKaWarps = 8, kKaGroups = kKaWarps / 4;
+constexpr int kKaMaxChunkBatch = 1024;      // sequences that the chunked way handles
+constexpr int kKaChunkMin = 16;             // blocks of a chunk, at least
 constexpr int kKaMaxCluster = 8;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -345,23 +351,25 @@ struct KaQuery {  // int8: sum_n 256^n digit_n; k-step j: b[.][2j], b[.][2j + 1]
   uint32_t b[kDigits][8];
 
   __device__ __forceinline__ float set(const uint32_t (&raw)[16], uint32_t e) {
-    // largest value to below 127/128 of 2^(8 kDigits - 1): every digit is a signed byte
-    constexpr float top = (kDigits == 2 ? 16384.f : 4194304.f) * (127.f / 128.f);
+    // largest value to below 127/128 of 2^15 (two digits) or 2^22 (three, the most
+    // that `magic` leaves room for): every digit is a signed byte
+    constexpr float top = (kDigits == 2 ? 16384.f : 2097152.f) * (127.f / 128.f);
+    constexpr float magic = 12582912.f;  // 1.5 * 2^23: its sum holds the rounded value in the low bits
+    constexpr uint32_t bias = kDigits == 2 ? 0x8080u : 0x808080u;
     const float dn = __uint_as_float((254u - e) << 23);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int n = 0; n < kDigits; ++n) b[n][i] = 0;
+      uint32_t u[4];  // byte n: digit n (v + bias has unsigned digits; each less 128 is signed)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t w = raw[2 * i + (k >> 1)];
-        int v = __float2int_rn(((k & 1) ? bf16_hi(w) : bf16_lo(w)) * dn * top);
+        const float y = fmaf(((k & 1) ? bf16_hi(w) : bf16_lo(w)) * dn, top, magic);
+        u[k] = (__float_as_uint(y) - __float_as_uint(magic) + bias) ^ bias;
+      }
 #pragma unroll
-        for (int n = 0; n < kDigits; ++n) {  // the lowest first
-          const int d = static_cast<int8_t>(v & 0xff);
-          b[n][i] |= static_cast<uint32_t>(d & 0xff) << (8 * k);
-          v = (v - d) >> 8;
-        }
+      for (int n = 0; n < kDigits; ++n) {
+        const uint32_t sel = 0x0040u + 0x0011u * n;  // byte n of both words
+        b[n][i] = __byte_perm(__byte_perm(u[0], u[1], sel), __byte_perm(u[2], u[3], sel), 0x5410);
       }
     }
     return __uint_as_float(e << 23) * (1.f / top);
@@ -660,17 +668,17 @@ __device__ __forceinline__ KaChunk find_chunk(const Kv8View& kv, int batch, int 
 __device__ __forceinline__ size_t chunk_floats(int G) { return static_cast<size_t>(G) * kDim + 2 * kMaxGroup + 4; }
 
 template <int CODE, bool F32OUT, bool CHUNKS>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(32 * kKaWarps, 2)
     kv8_attend_kernel(const __grid_constant__ Kv8AttendParams p) {
   // the warps' rings; once every block is used, the warps' partials
   extern __shared__ __align__(128) uint8_t smem_raw[];
   float* part = reinterpret_cast<float*>(smem_raw);
-  __shared__ float ml[kKaMaxWarps][2][kMaxGroup];
+  __shared__ float ml[kKaWarps][2][kMaxGroup];
   __shared__ float cta_ml[2][kMaxGroup];
   __shared__ int cta_bad;
   const int CS = CHUNKS ? 1 : static_cast<int>(gridDim.x), rank = CHUNKS ? 0 : static_cast<int>(blockIdx.x);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int threads = static_cast<int>(blockDim.x), n_warps = threads >> 5;
+  constexpr int threads = 32 * kKaWarps;
   const int G = p.G;
   const int quarter = warp & 3;
   griddep_launch_dependents();
@@ -695,7 +703,7 @@ __global__ void __launch_bounds__(256, 2)
   // first chunk's block numbers are read together with the length and the count
   // (inside the list's storage whatever those turn out to be).
   const int32_t* sel = !CHUNKS && p.sel_idx != nullptr ? p.sel_idx + static_cast<size_t>(pair) * p.max_sel : nullptr;
-  const int js = CS * (n_warps >> 2), grp = rank * (n_warps >> 2) + (warp >> 2);
+  const int js = CS * kKaGroups, grp = rank * kKaGroups + (warp >> 2);
   const int jb = CHUNKS ? ch.q * ch.size + grp : grp;
   const int L = p.kv.seq_lens[s];
   int m = 0, first_b = 0, first_next = 0, last_b = 0;
@@ -805,7 +813,8 @@ __global__ void __launch_bounds__(256, 2)
   const bool tail_turn = CHUNKS ? (ch.q == ch.chunks - 1 && grp == 0) : grp == (m - 1) % js;
   if (!bad && tail_turn && 16 * quarter < L - c * kBlock) {
     const size_t off = static_cast<size_t>(pair) * (kBlock * kDim);
-    attend_tail<F32OUT ? 3 : 2>(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * quarter, L - c * kBlock, p.scale_log2);
+    attend_tail<F32OUT ? 3 : 2>(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * quarter, L - c * kBlock,
+                                p.scale_log2);
   }
 
   // ---- the stored blocks
@@ -855,10 +864,12 @@ __global__ void __launch_bounds__(256, 2)
   for (int i = tid; i < G * kDim; i += threads) {
     const int hd = i / kDim, d = i % kDim;
     float top = ml[0][0][hd];
-    for (int w = 1; w < n_warps; ++w) top = fmaxf(top, ml[w][0][hd]);
+#pragma unroll
+    for (int w = 1; w < kKaWarps; ++w) top = fmaxf(top, ml[w][0][hd]);
     float o = 0.f, l = 0.f;
     const int at = (hd >> 1) * kKaHeadPair + (hd & 1) * kDim + d;
-    for (int w = 0; w < n_warps; ++w) {
+#pragma unroll
+    for (int w = 0; w < kKaWarps; ++w) {
       const float f = weight(ml[w][0][hd], top);
       o = fmaf(f, part[w * kKaPart + at], o);
       l = fmaf(f, ml[w][1][hd], l);
@@ -1026,18 +1037,14 @@ cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int 
                  : launch_pdl(kv8_read_kernel<kCodeInt8, __nv_bfloat16>, grid, 256, 0, stream, 0, p);
 }
 
-// Two groups a CTA (two such CTAs an SM), and as many CTAs a cluster as keep
-// the whole grid resident at once (2 x 148), up to one block a group.
-// Measured, (CTAs a cluster, groups) -> us: 64 pairs x 32 blocks (8, 1) 14.0,
-// (8, 2) 20.8, (4, 2) 11.7, (2, 2) 13.8; 256 pairs x 64 blocks (8, 1) 72.7,
-// (2, 2) 60.2, (1, 2) 53.4.
-Kv8AttendPlan kv8_attend_plan(int pairs, int max_blocks) {
-  Kv8AttendPlan a{};
-  a.groups = 2;
-  a.cluster = 1;
-  while (a.cluster < kKaMaxCluster && pairs * a.cluster * 2 <= 2 * 148 && a.cluster * 2 * a.groups <= max_blocks)
-    a.cluster *= 2;
-  return a;
+// CTAs of a cluster: as many as keep the whole grid resident at once (two of 8
+// warps an SM), up to one block a group of four warps.  Measured, CTAs a cluster
+// -> us: 64 pairs x 32 blocks 8 -> 20.8, 4 -> 11.7, 2 -> 13.8; 256 pairs x 64
+// blocks 8 -> 102, 4 -> 71, 2 -> 60, 1 -> 53.
+int kv8_attend_cluster(int pairs, int max_blocks) {
+  int cluster = 1;
+  while (cluster < kKaMaxCluster && pairs * cluster * 2 <= 2 * 148 && cluster * 2 * kKaGroups <= max_blocks) cluster *= 2;
+  return cluster;
 }
 
 // The grid holds target + pairs chunks at most.  Up to 74 pairs they all fit
@@ -1050,36 +1057,35 @@ size_t kv8_attend_scratch_bytes(long long pairs, int G) {
 
 cudaError_t launch_kv8_attend(int code, bool f32_out, Kv8AttendParams p, cudaStream_t stream) {
   const int pairs = p.batch * p.kv.hkv;
+  constexpr int T = 32 * kKaWarps;
+  constexpr size_t smem = kKaWarps * std::max(kKaStages * kKaSlot, kKaPart * 4);
   // Chunks where a sequence may be longer than a few of them and the workspace
   // holds their partial sums
   if (p.sel_idx == nullptr && p.ws_part != nullptr && p.batch <= kKaMaxChunkBatch && p.kv.blocks > 4 * kKaChunkMin) {
-    constexpr size_t smem = kKaMaxWarps * std::max(kKaStages * kKaSlot, kKaPart * 4);
     p.target = static_cast<int>(chunk_target(pairs));
     const dim3 grid(static_cast<unsigned>(p.target + pairs)), cgrid(static_cast<unsigned>(pairs), static_cast<unsigned>(p.G));
     cudaError_t e;
     if (code == kCodeE4m3)
-      e = f32_out ? launch_pdl(kv8_attend_kernel<kCodeE4m3, true, true>, grid, 256, smem, stream, 0, p)
-                  : launch_pdl(kv8_attend_kernel<kCodeE4m3, false, true>, grid, 256, smem, stream, 0, p);
+      e = f32_out ? launch_pdl(kv8_attend_kernel<kCodeE4m3, true, true>, grid, T, smem, stream, 0, p)
+                  : launch_pdl(kv8_attend_kernel<kCodeE4m3, false, true>, grid, T, smem, stream, 0, p);
     else
-      e = f32_out ? launch_pdl(kv8_attend_kernel<kCodeInt8, true, true>, grid, 256, smem, stream, 0, p)
-                  : launch_pdl(kv8_attend_kernel<kCodeInt8, false, true>, grid, 256, smem, stream, 0, p);
+      e = f32_out ? launch_pdl(kv8_attend_kernel<kCodeInt8, true, true>, grid, T, smem, stream, 0, p)
+                  : launch_pdl(kv8_attend_kernel<kCodeInt8, false, true>, grid, T, smem, stream, 0, p);
     if (e != cudaSuccess) return e;
     return f32_out ? launch_pdl(kv8_combine_kernel<true>, cgrid, 256, 0, stream, 0, p)
                    : launch_pdl(kv8_combine_kernel<false>, cgrid, 256, 0, stream, 0, p);
   }
-  const Kv8AttendPlan a = kv8_attend_plan(pairs, p.sel_idx != nullptr ? p.max_sel : p.kv.blocks);
-  const dim3 grid(static_cast<unsigned>(a.cluster), static_cast<unsigned>(pairs));
-  const int T = 128 * a.groups;
-  const size_t smem = static_cast<size_t>(4 * a.groups) * std::max(kKaStages * kKaSlot, kKaPart * 4);
+  const int cluster = kv8_attend_cluster(pairs, p.sel_idx != nullptr ? p.max_sel : p.kv.blocks);
+  const dim3 grid(static_cast<unsigned>(cluster), static_cast<unsigned>(pairs));
   if (code == kCodeE4m3)
-    return f32_out ? launch_pdl(kv8_attend_kernel<kCodeE4m3, true, false>, grid, T, smem, stream, a.cluster, p)
-                   : launch_pdl(kv8_attend_kernel<kCodeE4m3, false, false>, grid, T, smem, stream, a.cluster, p);
-  return f32_out ? launch_pdl(kv8_attend_kernel<kCodeInt8, true, false>, grid, T, smem, stream, a.cluster, p)
-                 : launch_pdl(kv8_attend_kernel<kCodeInt8, false, false>, grid, T, smem, stream, a.cluster, p);
+    return f32_out ? launch_pdl(kv8_attend_kernel<kCodeE4m3, true, false>, grid, T, smem, stream, cluster, p)
+                   : launch_pdl(kv8_attend_kernel<kCodeE4m3, false, false>, grid, T, smem, stream, cluster, p);
+  return f32_out ? launch_pdl(kv8_attend_kernel<kCodeInt8, true, false>, grid, T, smem, stream, cluster, p)
+                 : launch_pdl(kv8_attend_kernel<kCodeInt8, false, false>, grid, T, smem, stream, cluster, p);
 }
 
 cudaError_t prepare_kv8_kernels() {
-  constexpr int smem = kKaMaxWarps * std::max(kKaStages * kKaSlot, kKaPart * 4);
+  constexpr int smem = kKaWarps * std::max(kKaStages * kKaSlot, kKaPart * 4);
   for (auto* k : {kv8_attend_kernel<kCodeE4m3, false, false>, kv8_attend_kernel<kCodeE4m3, true, false>,
                   kv8_attend_kernel<kCodeInt8, false, false>, kv8_attend_kernel<kCodeInt8, true, false>,
                   kv8_attend_kernel<kCodeE4m3, false, true>, kv8_attend_kernel<kCodeE4m3, true, true>,
