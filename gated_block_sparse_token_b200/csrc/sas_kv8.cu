@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
   // positions begin .. end - 1, in blocks b0 .. b1 - 1
   const int end = err ? 0 : static_cast<int>(min(static_cast<long long>(begin) + p.count, static_cast<long long>(L)));
   if (o.data != nullptr && begin < end) {
-    const int c = (L - 1) / kBlock, b0 = begin / kBlock, b1 = (end - 1) / kBlock + 1, step = static_cast<int>(gridDim.x);
+    const int c = (L - 1) / kBlock, b0 = begin / kBlock, b1 = (end - 1) / kBlock + 1;
+    const int step = static_cast<int>(gridDim.x);
     const uint8_t* codes = half == 0 ? p.kv.k : p.kv.v;
     const float* scales = half == 0 ? p.kv.k_scale : p.kv.v_scale;
     const int d0 = VEC * (tid % LPR), r0 = tid / LPR;  // rows r0, r0 + ROWS, ..
@@ -581,8 +582,9 @@ __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint32_t sel = (j & 1) ? 0x7632 : 0x5410;
-    const uint32_t a0 = __byte_perm(v[0][j / 2], v[1][j / 2], sel), a1 = __byte_perm(v[0][4 + j / 2], v[1][4 + j / 2], sel);
-    const uint32_t a2 = __byte_perm(v[2][j / 2], v[3][j / 2], sel), a3 = __byte_perm(v[2][4 + j / 2], v[3][4 + j / 2], sel);
+    const int w = j / 2;
+    const uint32_t a0 = __byte_perm(v[0][w], v[1][w], sel), a1 = __byte_perm(v[0][4 + w], v[1][4 + w], sel);
+    const uint32_t a2 = __byte_perm(v[2][w], v[3][w], sel), a3 = __byte_perm(v[2][4 + w], v[3][4 + w], sel);
 #pragma unroll
     for (int n = 0; n < TERMS; ++n) mma_bf16_16816(st.acc[j], a0, a1, a2, a3, b[n][0], b[n][1]);
   }
@@ -912,26 +914,40 @@ __global__ void __launch_bounds__(32 * kKaWarps, 2)
   }
   // every CTA's partial is complete and visible to the cluster
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // all of an output's remote values are requested before the first is used (a
+  // rank past the cluster's reads the last one again, with weight 0)
   const int dpc = kDim / CS;
+  int bads[kKaMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kKaMaxCluster; ++r) bads[r] = __float_as_int(ld_dsmem(dsmem_addr(&cta_bad, min(r, CS - 1))));
   bool any_bad = false;
-  for (int r = 0; r < CS; ++r) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(dsmem_addr(&cta_bad, r)) : "memory");
-    any_bad = any_bad || v != 0;
-  }
   for (int i = tid; i < G * dpc; i += threads) {
     const int hd = i / dpc, d = rank * dpc + i % dpc;
     const int at = (hd >> 1) * kKaHeadPair + (hd & 1) * kDim + d;
-    float top = -INFINITY;
-    for (int r = 0; r < CS; ++r) top = fmaxf(top, ld_dsmem(dsmem_addr(&cta_ml[0][hd], r)));
+    float ms[kKaMaxCluster], ls[kKaMaxCluster], os[kKaMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kKaMaxCluster; ++r) {
+      ms[r] = ld_dsmem(dsmem_addr(&cta_ml[0][hd], min(r, CS - 1)));
+      ls[r] = ld_dsmem(dsmem_addr(&cta_ml[1][hd], min(r, CS - 1)));
+      os[r] = ld_dsmem(dsmem_addr(part + at, min(r, CS - 1)));
+    }
+    any_bad = false;
+    float top = ms[0];
+#pragma unroll
+    for (int r = 0; r < kKaMaxCluster; ++r) {
+      any_bad = any_bad || bads[r] != 0;
+      top = fmaxf(top, ms[r]);
+    }
     float o = 0.f, l = 0.f;
-    for (int r = 0; r < CS; ++r) {
-      const float f = weight(ld_dsmem(dsmem_addr(&cta_ml[0][hd], r)), top);
-      o = fmaf(f, ld_dsmem(dsmem_addr(part + at, r)), o);
-      l = fmaf(f, ld_dsmem(dsmem_addr(&cta_ml[1][hd], r)), l);
+#pragma unroll
+    for (int r = 0; r < kKaMaxCluster; ++r) {
+      const float f = weight(ms[r], top);
+      o = r < CS ? fmaf(f, os[r], o) : o;
+      l = r < CS ? fmaf(f, ls[r], l) : l;
     }
     store(hd, d, any_bad ? 0.f : o / l);
   }
+  // (thread 0 has an output in every CTA)
   if (any_bad && rank == 0 && tid == 0) raise_status(p.status, kStatusBounds);
   // no CTA leaves while another may still read its shared memory
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -1043,7 +1059,8 @@ cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int 
 // blocks 8 -> 102, 4 -> 71, 2 -> 60, 1 -> 53.
 int kv8_attend_cluster(int pairs, int max_blocks) {
   int cluster = 1;
-  while (cluster < kKaMaxCluster && pairs * cluster * 2 <= 2 * 148 && cluster * 2 * kKaGroups <= max_blocks) cluster *= 2;
+  while (cluster < kKaMaxCluster && pairs * cluster * 2 <= 2 * 148 && cluster * 2 * kKaGroups <= max_blocks)
+    cluster *= 2;
   return cluster;
 }
 
@@ -1063,7 +1080,8 @@ cudaError_t launch_kv8_attend(int code, bool f32_out, Kv8AttendParams p, cudaStr
   // holds their partial sums
   if (p.sel_idx == nullptr && p.ws_part != nullptr && p.batch <= kKaMaxChunkBatch && p.kv.blocks > 4 * kKaChunkMin) {
     p.target = static_cast<int>(chunk_target(pairs));
-    const dim3 grid(static_cast<unsigned>(p.target + pairs)), cgrid(static_cast<unsigned>(pairs), static_cast<unsigned>(p.G));
+    const dim3 grid(static_cast<unsigned>(p.target + pairs));
+    const dim3 cgrid(static_cast<unsigned>(pairs), static_cast<unsigned>(p.G));
     cudaError_t e;
     if (code == kCodeE4m3)
       e = f32_out ? launch_pdl(kv8_attend_kernel<kCodeE4m3, true, true>, grid, T, smem, stream, 0, p)

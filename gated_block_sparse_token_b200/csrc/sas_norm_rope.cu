@@ -65,7 +65,8 @@ __device__ __forceinline__ float sum8lanes(float v) {
 // blockIdx.y: a chunk of p.chunk heads, the query heads' chunks first (a
 // chunk never mixes queries and keys); blockIdx.x: tokens, 32 at a time.
 template <typename T, bool kBack>
-__global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4)
+    norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, j = lane & 7;
@@ -231,7 +232,8 @@ cudaError_t launch_norm_rope(bool f32, bool back, NormRopeParams p, float* dgamm
   e = f32 ? launch_pdl(norm_rope_kernel<float, true>, grid, kNrThreads, 0, stream, 0, p)
           : launch_pdl(norm_rope_kernel<__nv_bfloat16, true>, grid, kNrThreads, 0, stream, 0, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_rope_gain_kernel, dim3(kDim / 32, 2), 1024, 0, stream, 0, p.ws_part, g.q_chunks * g.x, g.k_chunks * g.x, dgamma_q, dgamma_k);
+  return launch_pdl(norm_rope_gain_kernel, dim3(kDim / 32, 2), 1024, 0, stream, 0, p.ws_part, g.q_chunks * g.x,
+                    g.k_chunks * g.x, dgamma_q, dgamma_k);
 }
 
 }  // namespace sas

@@ -638,8 +638,9 @@ cudaError_t launch_pool_project_kv8(int code, const PoolParams& p, const CUtenso
                                     cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((p.num_blocks + kPpRows - 1) / kPpRows), static_cast<unsigned>(p.hkv),
                   static_cast<unsigned>(batch));
-  return code == kCodeE4m3 ? launch_pdl(pool_project_kernel<kSrcE4m3>, grid, pp_threads(kSrcE4m3), kPpSmem, stream, 0, p, tmwk)
-                           : launch_pdl(pool_project_kernel<kSrcInt8>, grid, pp_threads(kSrcInt8), kPpSmem, stream, 0, p, tmwk);
+  constexpr int T = pp_threads(kSrcE4m3);
+  return code == kCodeE4m3 ? launch_pdl(pool_project_kernel<kSrcE4m3>, grid, T, kPpSmem, stream, 0, p, tmwk)
+                           : launch_pdl(pool_project_kernel<kSrcInt8>, grid, T, kPpSmem, stream, 0, p, tmwk);
 }
 
 // ---------------------------------------------------------------- few blocks
@@ -747,11 +748,11 @@ cudaError_t launch_pool_few_kv8(int code, const PoolParams& p, int batch, cudaSt
 }
 
 cudaError_t prepare_pool_project_kernel() {
-  cudaError_t e = cudaFuncSetAttribute(pool_project_kernel<kSrcBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(pool_project_kernel<kSrcE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(pool_project_kernel<kSrcInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
+  for (auto* k : {pool_project_kernel<kSrcBf16>, pool_project_kernel<kSrcE4m3>, pool_project_kernel<kSrcInt8>}) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPpSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace sas
