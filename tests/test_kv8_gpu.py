@@ -287,8 +287,31 @@ def test_attend_groups(code, out, G):
     check_attend(kv, cfg, G, lists, q, o, lens)
 
 
+@pytest.mark.parametrize("B", [3, 40, 100, 200])   # clusters of 8, 4, 2 and 1
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_attend_cluster_sizes(B, out):
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(1, 64 * 40, (B,), generator=g).tolist()
+    lens[0], lens[1] = 64 * 40, 1
+    code = K.INT8 if B % 3 else K.E4M3
+    cfg = sas.Config(5, 1, token_budget=64 * 24, out_dtype=out)
+    kv = K.make_cache(B, 1, 40, code, True, lens, DEV, seed=B)
+    ws = ws_for(cfg)
+    lists = random_lists(lens, 1, 24, 8)
+    q, o = run_attend(kv, cfg, 5, lists, ws)
+    assert ok(ws)
+    q2, o2 = run_attend(kv, cfg, 5, lists, ws)
+    assert torch.equal(o, o2)
+    keep = [0, 1] + torch.randperm(B, generator=g)[:20].tolist()
+    for s in keep:
+        want, size = K.attend(kv, q, s, 0, 5, lists[s][0], lens[s], cfg.attn_scale)
+        tol = (2.0 ** -15 if out == "f32" else 2.0 ** -11 + 2.0 ** -13) * size
+        tol = tol + (2.0 ** -23 if out == "f32" else 2.0 ** -8) * want.abs()
+        assert bool(((o[s].cpu().double() - want).abs() <= tol).all()), s
+
+
 @pytest.mark.parametrize("code", CODES)
-@pytest.mark.parametrize("budget", [64, 128, 1024, 4096, 16384])
+@pytest.mark.parametrize("budget", [64, 128, 192, 1024, 4096, 16384])
 def test_attend_budgets(code, budget):
     lens = [64 * 300 + 31, 40, 64 * 70]
     cfg = sas.Config(4, 1, token_budget=budget)
@@ -414,6 +437,26 @@ def test_attend_reports_bad_lists_and_pages():
             else:
                 want, size = K.attend(kv, q, s, h, 2, lists[s][h], lens[s], cfg.attn_scale)
                 assert bool(((got.cpu().double() - want).abs() <= 2.0 ** -10 * size + 2.0 ** -8 * want.abs()).all())
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_poisoned_and_masked_values(code):
+    """A listed block with scale NaN makes its (sequence, head) NaN and no other; NaN in stale tail rows, in blocks
+    that are not listed and in other sequences' pages does not."""
+    lens = [900, 900]
+    cfg = sas.Config(4, 2, token_budget=256)
+    kv = K.make_cache(2, 2, 15, code, True, lens, DEV, seed=1)
+    lists = [[[1, 5, 9, 14], [0, 2, 3, 14]], [[1, 5, 9, 14], [0, 2, 3, 14]]]
+    kv.k_scale[kv.block_table[0, 5].long(), 0] = float("nan")        # listed by (0, 0) alone
+    kv.v_scale[kv.block_table[1, 4].long()] = float("nan")           # listed by none
+    ws = ws_for(cfg)
+    q, o = run_attend(kv, cfg, 2, lists, ws)
+    assert ok(ws)
+    assert bool(o[0, :2].isnan().all())
+    for s, h in ((0, 1), (1, 0), (1, 1)):
+        want, size = K.attend(kv, q, s, h, 2, lists[s][h], 900, cfg.attn_scale)
+        got = o[s, 2 * h:2 * h + 2].cpu().double()
+        assert bool(((got - want).abs() <= (2.0 ** -11 + 2.0 ** -13) * size + 2.0 ** -8 * want.abs()).all()), (s, h)
 
 
 def test_append_reports_bad_sequences():

@@ -125,6 +125,36 @@ def test_in_place_one_side_and_default_positions():
     assert torch.equal(only, want_k) and torch.equal(q, want_q) and torch.equal(k, want_k)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradient_in_place_and_one_side(dt):
+    """dx over dy and over x; keys alone; broadcast (stride 0) upstream gradients."""
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    q, k, gq, gk, g = _inputs(2, 50, 4, 2, dtype, "packed", 6)
+    cfg = sas.Config(4, 2, kv_dtype=dt)
+    dyq, dyk = torch.randn(q.shape, generator=g).to(dtype).to(DEV), torch.randn(k.shape, generator=g).to(dtype).to(DEV)
+    ws = torch.zeros(sas.qk_norm_rope_workspace_bytes(), dtype=torch.uint8, device=DEV)
+
+    def run(dyq, dyk, q, k, dq, dk):
+        dg = torch.zeros(2, 128, device=DEV)
+        sas.qk_norm_rope_backward(cfg, dyq, dyk, q, k, gq if q is not None else None, gk, dq, dk,
+                                  dg[0] if q is not None else None, dg[1], 1e6, ws)
+        return dg
+    wq, wk = torch.empty_like(q), torch.empty_like(k)
+    want = run(dyq, dyk, q, k, wq, wk)
+    only = torch.empty_like(k)
+    dg = run(None, dyk, None, k, None, only)
+    assert torch.equal(only, wk) and torch.equal(dg[1], want[1]) and float(dg[0].abs().max()) == 0
+    a, b = dyq.clone(), k.clone()
+    dg = run(a, dyk, q, b, a, b)
+    assert torch.equal(a, wq) and torch.equal(b, wk) and torch.equal(dg, want)
+    one = torch.randn(1, 1, 1, 128, generator=g).to(dtype).to(DEV)
+    x, y = torch.empty_like(q), torch.empty_like(k)
+    dg = run(one.expand(q.shape), one.expand(k.shape), q, k, x, y)
+    x2, y2 = torch.empty_like(q), torch.empty_like(k)
+    dg2 = run(one.expand(q.shape).contiguous(), one.expand(k.shape).contiguous(), q, k, x2, y2)
+    assert torch.equal(x, x2) and torch.equal(y, y2) and torch.equal(dg, dg2)
+
+
 def test_zero_rows_and_empty_batch():
     """A zero row stays zero (eps carries the norm); an empty batch does nothing."""
     cfg = sas.Config(2, 1)
