@@ -40,7 +40,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // dims per thread in registers between the maximum and the rounding, so a block
 // is read once and its codes written once; the next block's loads go out as
 // soon as the codes are made.  CTA 0 also writes the tail, after its first block
-// has read the tail's old rows.
+// has read the tail's old rows.  Bound by memory, 3 B a value: 156 MB of packed
+// tokens in 32-33 us (4.8 TB/s; their 256-byte rows lie 4 KiB apart), one CTA a
+// block 39; one token of each of 32 sequences 4.6 us, which is latency.
 __device__ __forceinline__ uint4 load_new_row(const RowsView& r, long long tok, int h, int s, int d0) {
   const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(r.data) + static_cast<long long>(s) * r.seq +
                            tok * r.token + static_cast<long long>(h) * r.head + d0;
@@ -161,7 +163,8 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const __grid_constan
 // A CTA walks every gridDim.x-th block of one (sequence, KV head)'s range,
 // threads 0-127 the keys, 128-255 the values.  A lane turns as many codes as
 // make 16 output bytes, so that a warp's stores fill whole sectors; the next
-// block's codes are requested before this one's values are stored.
+// block's codes are requested before this one's values are stored.  Bound by
+// memory, 3 B a value into bf16: 805 MB in 129 us (6.2 TB/s).
 template <int CODE, typename OutT>
 __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
   constexpr int VEC = 16 / static_cast<int>(sizeof(OutT));  // codes of a lane: 8 or 4

@@ -15,7 +15,10 @@
 // exchange and the mean one 8-lane reduction (three shuffles).  An 8-lane group
 // keeps its token's 8 (cos, sin) pairs in registers over a chunk of heads:
 // the angles are reduced in double precision (exact for any int32 position)
-// and would otherwise cost more than the row.
+// and would otherwise cost more than the row.  Measured, bf16, 32 + 8 heads:
+// 2 x 32,768 tokens 227 us (5.9 TB/s), one decode step of 8 sequences 2.5 us;
+// gradient of 8 x 1,021 padded tokens of 40 + 8 heads 45 us (5.0 TB/s) and 3 for
+// the gains' sum.
 #include "sas_internal.h"
 
 namespace sas {

@@ -522,6 +522,10 @@ SAS_API sas_status sas_qk_norm_rope_backward(const sas_config* cfg, const sas_ro
  * complete or not -- is kept in bf16 in the sequence's tail and is read from
  * there.  A block is quantised once, when it completes, from its bf16 values:
  * the cache's contents do not depend on how the tokens were split over calls.
+ * Lengths grow by sas_kv8_append; a sequence may be cut back within its current
+ * block (its tail still holds the rest), not into an earlier one.  A sequence
+ * may start on pages that another one completed, at a multiple of 64 tokens, and
+ * is read once it has appended a token of its own.
  * The release pages have no counterpart.
  */
 typedef enum { SAS_KV8_E4M3 = 0, SAS_KV8_INT8 = 1 } sas_kv8_code;
