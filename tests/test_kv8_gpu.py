@@ -95,6 +95,34 @@ def test_append_any_split(code, paged, chunks):
                 assert torch.equal(kept[0].view(torch.int16), kept[1].view(torch.int16))
 
 
+def test_shared_prefix_and_cutting_back():
+    """A sequence that starts on another's completed pages, and one cut back within its current block, go on as if
+    they had been written alone."""
+    cfg = sas.Config(2, 1)
+    kv = K.make_cache(2, 1, 5, K.E4M3, True, [1, 1], DEV, seed=8, spare=1)
+    ws = ws_for(cfg)
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(1, 1, 200, 128, generator=g).bfloat16()
+    y = torch.randn(1, 1, 80, 128, generator=g).bfloat16()
+    one = lambda n: torch.tensor(n, dtype=torch.int32, device=DEV)  # noqa: E731
+
+    def append(rows, lens, new, starts):
+        kv.seq_lens.copy_(one(lens))
+        r = rows.to(DEV)
+        sas.kv8_append(cfg, kv, r, r, ws, new_starts=one(starts), new_lens=one(new), max_new=max(new))
+    append(x, [200, 0], [200, 0], [0, 0])
+    append(x[:, :, :7], [195 + 7, 0], [7, 0], [0, 0])                # cut back to 195, seven more
+    kv.block_table[1, :2] = kv.block_table[0, :2]                    # the first two pages of sequence 0
+    append(y, [202, 128 + 80], [0, 80], [0, 0])
+    assert ok(ws)
+    a = torch.cat([x[0, 0, :195], x[0, 0, :7]])
+    b = torch.cat([x[0, 0, :128], y[0, 0]])
+    check_history(kv, [a[None], b[None]], [a[None], b[None]], [202, 208], K.E4M3)
+    q, o = run_attend(kv, cfg, 2, None, ws)
+    assert ok(ws)
+    check_attend(kv, cfg, 2, None, q, o, [202, 208])
+
+
 def test_append_padded_batch_strided_rows():
     """[B][Hkv][T][128] inputs (views of a packed projection), max_new for all."""
     B, hkv, T_ = 2, 3, 77
