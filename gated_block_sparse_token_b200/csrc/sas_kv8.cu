@@ -1059,9 +1059,14 @@ cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int 
 // CTAs of a cluster: as many as keep the whole grid resident at once (two of 8
 // warps an SM), up to one block a group of four warps.  Measured, CTAs a cluster
 // -> us: 64 pairs x 32 blocks 8 -> 20.8, 4 -> 11.7, 2 -> 13.8; 256 pairs x 64
-// blocks 8 -> 102, 4 -> 71, 2 -> 60, 1 -> 53.
+// blocks 8 -> 102, 4 -> 71, 2 -> 60, 1 -> 53.  More pairs than that run in waves:
+// two CTAs a pair shorten a last wave that is half empty or more (304 / 336 / 400
+// pairs x 64 blocks: 68 / 75 / 82 us against 72 / 83 / 86 with one; 512 and 592:
+// 103 and 118 against 98 and 115).
 int kv8_attend_cluster(int pairs, int max_blocks) {
   int cluster = 1;
+  const int last = pairs % (2 * 148);
+  if (pairs > 2 * 148 && last > 0 && last <= 148 && max_blocks >= 2 * kKaGroups) return 2;
   while (cluster < kKaMaxCluster && pairs * cluster * 2 <= 2 * 148 && cluster * 2 * kKaGroups <= max_blocks)
     cluster *= 2;
   return cluster;

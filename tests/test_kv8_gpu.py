@@ -315,7 +315,7 @@ def test_attend_groups(code, out, G):
     check_attend(kv, cfg, G, lists, q, o, lens)
 
 
-@pytest.mark.parametrize("B", [3, 40, 100, 200])   # clusters of 8, 4, 2 and 1
+@pytest.mark.parametrize("B", [3, 40, 100, 200, 300])   # clusters of 8, 4, 2, 1 and 2
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_attend_cluster_sizes(B, out):
     g = torch.Generator().manual_seed(B)
