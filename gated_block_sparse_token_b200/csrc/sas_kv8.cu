@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
   const int L = p.kv.seq_lens[s];
   const int begin = p.begin != nullptr ? p.begin[s] : 0;
   const RowsView o = half == 0 ? p.k_out : p.v_out;
-  bool err = L < 1 || begin < 0 || static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
+  bool err = L < 0 || begin < 0 || static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
   // positions begin .. end - 1, in blocks b0 .. b1 - 1
   const int end = err ? 0 : static_cast<int>(min(static_cast<long long>(begin) + p.count, static_cast<long long>(L)));
   if (o.data != nullptr && begin < end) {

@@ -544,7 +544,9 @@ typedef struct {
                                  page ids (the current block needs one only
                                  once it completes) */
   const int32_t* seq_lens;    /* [B] tokens of each sequence, including those
-                                 that the call appends */
+                                 that the call appends; 0 (an empty slot) is
+                                 accepted by every call but the attention,
+                                 which wants 1 or more as sas_kv does */
   int32_t batch;              /* B >= 0 (0: nothing to do) */
   int32_t capacity;           /* contiguous: tokens per (seq, head), multiple of 64 */
   int32_t num_pages;
@@ -579,7 +581,7 @@ SAS_API sas_status sas_kv8_append(const sas_config* cfg, const sas_kv8* kv, cons
  * the tail's value, rounded to out_dtype.  Rows at or past the sequence's
  * length stay as they were.  Either output may be NULL.  A token whose page is
  * out of range reads as 0 and is reported as SAS_ERR_DEVICE_BOUNDS; a sequence
- * with a length or begin out of range is skipped and reported.
+ * with a length (0 is none) or begin out of range is skipped and reported.
  *   cfg           num_kv_heads, out_dtype (bf16 or fp32, of the outputs)
  *   k_out, v_out  rows [B][Hkv][count]
  */

@@ -201,6 +201,32 @@ def test_read_back(code, paged, out):
                     assert bool((got[s, h, want.shape[0]:] == 9.0).all())
 
 
+def test_empty_slots():
+    """Length 0: append with nothing new, read-back and pooling leave the slot alone and report nothing; the
+    attention, like the bf16 one, reports it and zeroes its output."""
+    cfg = sas.Config(2, 1)
+    kv = K.make_cache(3, 1, 4, K.INT8, True, [130, 1, 64], DEV, seed=4)
+    kv.seq_lens[1] = 0
+    ws = ws_for(cfg)
+    x = torch.zeros(3, 1, 1, 128, dtype=torch.bfloat16, device=DEV)
+    before = [t.clone() for t in (kv.k, kv.k_tail.view(torch.int16), kv.k_scale)]
+    sas.kv8_append(cfg, kv, x, x, ws, new_lens=torch.zeros(3, dtype=torch.int32, device=DEV))
+    out = torch.full((3, 1, 130, 128), 5.0, dtype=torch.bfloat16, device=DEV)
+    sas.kv8_read(cfg, kv, out, None, ws)
+    gk = torch.full((3, 1, 4, 128), 5.0, device=DEV)
+    sas.pool_keys_kv8(cfg, kv, torch.zeros(1, 384, 128, dtype=torch.bfloat16, device=DEV), torch.ones(128, device=DEV),
+                      gk, ws)
+    assert ok(ws) and bool((out[1] == 5).all()) and bool((gk[1] == 5).all())
+    assert torch.equal(kv.k, before[0]) and torch.equal(kv.k_tail.view(torch.int16), before[1])
+    assert torch.equal(kv.k_scale, before[2])
+    q, o = run_attend(kv, cfg, 2, None, ws)
+    torch.cuda.synchronize()
+    assert sas.get_device_status(ws) == sas.SAS_ERR_DEVICE_BOUNDS and float(o[1].float().abs().max()) == 0
+    for s, L in ((0, 130), (2, 64)):
+        want, size = K.attend(kv, q, s, 0, 2, list(range((L - 1) // 64 + 1)), L, cfg.attn_scale)
+        assert bool(((o[s].cpu().double() - want).abs() <= 2.0 ** -10 * size + 2.0 ** -8 * want.abs()).all())
+
+
 # ---------------------------------------------------------------- gate keys
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("paged", [False, True])
