@@ -40,9 +40,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // dims per thread in registers between the maximum and the rounding, so a block
 // is read once and its codes written once; the next block's loads go out as
 // soon as the codes are made.  CTA 0 also writes the tail, after its first block
-// has read the tail's old rows.  Bound by memory, 3 B a value: 156 MB of packed
-// tokens in 32-33 us (4.8 TB/s; their 256-byte rows lie 4 KiB apart), one CTA a
-// block 39; one token of each of 32 sequences 4.6 us, which is latency.
+// has read the tail's old rows.  Bound by memory, 3 B a value: 4 x 32,768 packed
+// tokens 129 us (6.3 TB/s), six ragged chunks of 1,219 to 8,190 tokens 30-33 us
+// (one CTA a block: 39); one token of each of 32 sequences 4.6 us, which is latency.
 __device__ __forceinline__ uint4 load_new_row(const RowsView& r, long long tok, int h, int s, int d0) {
   const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(r.data) + static_cast<long long>(s) * r.seq +
                            tok * r.token + static_cast<long long>(h) * r.head + d0;
