@@ -235,8 +235,10 @@ cudaError_t launch_norm_rope(bool f32, bool back, NormRopeParams p, float* dgamm
   e = f32 ? launch_pdl(norm_rope_kernel<float, true>, grid, kNrThreads, 0, stream, 0, p)
           : launch_pdl(norm_rope_kernel<__nv_bfloat16, true>, grid, kNrThreads, 0, stream, 0, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_rope_gain_kernel, dim3(kDim / 32, 2), 1024, 0, stream, 0, p.ws_part, g.q_chunks * g.x,
-                    g.k_chunks * g.x, dgamma_q, dgamma_k);
+  int q_rows = g.q_chunks * g.x, k_rows = g.k_chunks * g.x;
+  if (dgamma_q == dgamma_k && p.hq > 0 && p.hkv > 0) q_rows += k_rows, k_rows = 0;  // one gain: one sum
+  return launch_pdl(norm_rope_gain_kernel, dim3(kDim / 32, 2), 1024, 0, stream, 0, p.ws_part, q_rows, k_rows, dgamma_q,
+                    dgamma_k);
 }
 
 }  // namespace sas

@@ -494,7 +494,8 @@ SAS_API size_t sas_qk_norm_rope_workspace_bytes(void);
  * (rows, kv_dtype), writes dq = dL/dq and dk = dL/dk (rows, kv_dtype; they may
  * be dq_out and dk_out or q and k themselves) and ADDS to dgamma_q, dgamma_k
  * (fp32 [128]; zero them first for a fresh gradient; fixed order of summation,
- * repeated calls add identical values).  q, k are the forward's inputs.  Rows
+ * repeated calls add identical values; one buffer for both, for a gain that
+ * queries and keys share, gets the sum).  q, k are the forward's inputs.  Rows
  * with a negative position are skipped and contribute nothing.  Queries or
  * keys may be left out as in the forward (all of their pointers NULL).
  *   ws  at least sas_qk_norm_rope_workspace_bytes() bytes, 16-byte aligned

@@ -155,6 +155,23 @@ def test_gradient_in_place_and_one_side(dt):
     assert torch.equal(x, x2) and torch.equal(y, y2) and torch.equal(dg, dg2)
 
 
+def test_one_gain_for_queries_and_keys():
+    """One gain and one gradient buffer for both sides: the buffer gets the sum of the two."""
+    B, T, hq, hkv = 2, 700, 16, 4
+    q, k, gain, _, g = _inputs(B, T, hq, hkv, torch.bfloat16, "packed", 7)
+    cfg = sas.Config(hq, hkv, norm_eps=EPS)
+    dyq, dyk = torch.randn(q.shape, generator=g).bfloat16().to(DEV), torch.randn(k.shape, generator=g).bfloat16().to(DEV)
+    ws = torch.zeros(sas.qk_norm_rope_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    pos = torch.arange(T, dtype=torch.int32).expand(B, T)
+    sides = [K.norm_rope_grad(x.cpu(), gain.cpu(), pos, 1e4, EPS, dy.cpu()) for x, dy in ((q, dyq), (k, dyk))]
+    want, size = sides[0][2] + sides[1][2], sides[0][3] + sides[1][3]
+    for _ in range(3):
+        dg = torch.ones(128, device=DEV)
+        sas.qk_norm_rope_backward(cfg, dyq, dyk, q, k, gain, gain, torch.empty_like(q), torch.empty_like(k), dg, dg,
+                                  1e4, ws)
+        assert bool(((dg.cpu().double() - 1 - want).abs() <= 2.0 ** -17 * (size + 1)).all())
+
+
 def test_zero_rows_and_empty_batch():
     """A zero row stays zero (eps carries the norm); an empty batch does nothing."""
     cfg = sas.Config(2, 1)
