@@ -291,14 +291,18 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 //                m16n8k32 with the query as two e4m3 terms ran slower than the
 //                conversions it saves: 144 us against 114 for 2 x 128k tokens.)
 //   softmax      per head over the columns, fp32, base 2; the running maximum
-//                moves only when it grows by more than 2^8 (any factor common
-//                to p and its sum cancels), so most blocks need one vote and
-//                no shuffles;
+//                moves only when it grows by more than 2^kKaGrow (any factor
+//                common to p and its sum cancels), so most blocks need one vote
+//                and no shuffles;
 //   O^T += V^T P^T  m16n8k16 f16 (codes are exact in f16), the P fragment
-//                transposed in place by movmatrix.  P is rounded to f16 (2^-11
-//                relative, before a bf16 output); for an fp32 output a second
-//                product carries the remainder.  The sum of P runs over the
-//                unrounded values.
+//                transposed in place by movmatrix.  P is rounded to f16 (before a
+//                bf16 output); for an fp32 output a second product carries the
+//                remainder.  It enters as 2^kKaShift p, so that the rounding is
+//                2^-11 relative for every key down to 2^-25 of the largest: a few
+//                keys that take nearly all the weight leave the others exact
+//                enough (unshifted, a hundred thousand keys at 2^-24 were a third
+//                off).  V's scale takes the factor back.  The sum of P runs over
+//                the unrounded values.
 // Both products take their k index from whatever order makes a lane's 16-byte
 // shared load its fragment: dims 16t .. 16t+15 and 64 + those for K, dims 16g ..
 // of four keys for V.  Key g of a fragment is row 2(g/2) + g/4 (xor 4 for odd
@@ -326,6 +330,8 @@ constexpr int kKaWarps = 8, kKaGroups = kKaWarps / 4;
 constexpr int kKaMaxChunkBatch = 1024;      // sequences that the chunked way handles
 constexpr int kKaChunkMin = 16;             // blocks of a chunk, at least
 constexpr int kKaMaxCluster = 8;
+// p <= 2^(kKaShift + kKaGrow) stays below f16's largest value
+constexpr float kKaGrow = 4.f, kKaShift = 11.f, kKaUnshift = 1.f / 2048.f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -347,8 +353,12 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 }
 
 // The query of one head (this lane: 32 of its values as 16 bf16 pairs) as B
-// fragments; set() takes the biased exponent e (1 .. 253) of the head's largest
+// fragments; set() takes the biased exponent e (1 .. 254) of the head's largest
 // value and returns the unit that the fragments count in.
+__device__ __forceinline__ float pow2_down(uint32_t e) {  // 2^(127 - e), e = 254: below the normal range
+  return __uint_as_float(e < 254u ? (254u - e) << 23 : 0x00400000u);
+}
+
 template <int CODE, bool F32OUT>
 struct KaQuery {  // int8: sum_n 256^n digit_n; k-step j: b[.][2j], b[.][2j + 1]
   static constexpr int kDigits = F32OUT ? 3 : 2;
@@ -360,7 +370,7 @@ struct KaQuery {  // int8: sum_n 256^n digit_n; k-step j: b[.][2j], b[.][2j + 1]
     constexpr float top = (kDigits == 2 ? 16384.f : 2097152.f) * (127.f / 128.f);
     constexpr float magic = 12582912.f;  // 1.5 * 2^23: its sum holds the rounded value in the low bits
     constexpr uint32_t bias = kDigits == 2 ? 0x8080u : 0x808080u;
-    const float dn = __uint_as_float((254u - e) << 23);
+    const float dn = pow2_down(e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t u[4];  // byte n: digit n (v + bias has unsigned digits; each less 128 is signed)
@@ -384,7 +394,7 @@ struct KaQuery<kCodeE4m3, F32OUT> {  // f16; k-step j: b[2j], b[2j + 1]
   uint32_t b[16];
 
   __device__ __forceinline__ float set(const uint32_t (&raw)[16], uint32_t e) {
-    const float dn = __uint_as_float((254u - e) << 23);  // q 2^(127 - e) lies in [0, 4)
+    const float dn = pow2_down(e);  // q dn lies in (-2, 2)
 #pragma unroll
     for (int i = 0; i < 16; ++i) b[i] = pack_f16x2(bf16_lo(raw[i]) * dn, bf16_hi(raw[i]) * dn);
     return __uint_as_float(e << 23);
@@ -410,7 +420,7 @@ __device__ __forceinline__ float ld_dsmem(uint32_t addr) {
 }
 
 struct KaState {
-  float m[2], l[2];   // heads 2t, 2t + 1 (m in the base-2 logit domain, uniform over g)
+  float m[2], l[2];   // heads 2t, 2t + 1 (m: base-2 logit, the maximum within 2^kKaGrow, less kKaShift; uniform over g)
   float acc[8][4];    // O^T: dims 16g + j (0, 1) and 16g + 8 + j (2, 3), heads 2t, 2t + 1
 };
 
@@ -419,7 +429,8 @@ __device__ __forceinline__ float weight(float m, float top) { return m == -INFIN
 // Moves the running maximum to cover the 16 x 8 logits sc (this lane: keys
 // g, g + 8 x heads 2t, 2t + 1).
 __device__ __forceinline__ void raise_max(KaState& st, const float (&sc)[4]) {
-  const bool grow = fmaxf(sc[0], sc[2]) > st.m[0] + 8.f || fmaxf(sc[1], sc[3]) > st.m[1] + 8.f;
+  constexpr float room = kKaShift + kKaGrow;
+  const bool grow = fmaxf(sc[0], sc[2]) > st.m[0] + room || fmaxf(sc[1], sc[3]) > st.m[1] + room;
   if (!__any_sync(0xffffffffu, grow)) return;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -427,7 +438,7 @@ __device__ __forceinline__ void raise_max(KaState& st, const float (&sc)[4]) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-    const float top = fmaxf(st.m[e], x);
+    const float top = fmaxf(st.m[e], x - kKaShift);
     const float f = weight(st.m[e], top);
     st.m[e] = top;
     st.l[e] *= f;
@@ -509,14 +520,15 @@ __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint
       }
   }
   const float f0 = qs[0] * ks, f1 = qs[1] * ks;
+  vs *= kKaUnshift;
 #pragma unroll
   for (int e = 0; e < 4; ++e) sc[e] *= (e & 1) ? f1 : f0;
   raise_max(st, sc);
   float p[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) p[e] = exp2_approx(sc[e] - st.m[e & 1]);
-  st.l[0] += p[0] + p[2];
-  st.l[1] += p[1] + p[3];
+  st.l[0] = fmaf(p[0] + p[2], kKaUnshift, st.l[0]);
+  st.l[1] = fmaf(p[1] + p[3], kKaUnshift, st.l[1]);
   const uint32_t h0 = pack_f16x2(p[0], p[1]), h1 = pack_f16x2(p[2], p[3]);
   const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
   uint32_t e0 = 0, e1 = 0;
@@ -561,7 +573,7 @@ __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt
   raise_max(st, sc);
   float p[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) p[e] = (e < 2 ? in0 : in1) ? exp2_approx(sc[e] - st.m[e & 1]) : 0.f;
+  for (int e = 0; e < 4; ++e) p[e] = (e < 2 ? in0 : in1) ? exp2_approx(sc[e] - (st.m[e & 1] + kKaShift)) : 0.f;
   st.l[0] += p[0] + p[2];
   st.l[1] += p[1] + p[3];
   uint32_t b[TERMS][2];
@@ -796,7 +808,7 @@ __global__ void __launch_bounds__(32 * kKaWarps, 2)
     mag = max(mag & 0xffffu, mag >> 16);
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-    float unit = qf.set(raw, min(max(mag >> 7, 1u), 253u));
+    float unit = qf.set(raw, min(max(mag >> 7, 1u), 254u));
     if (mag >= kBf16Inf) unit = __uint_as_float(0x7fc00000u);  // an infinity or NaN: every logit is NaN
     qs[0] = __shfl_sync(0xffffffffu, unit, 8 * t) * p.scale_log2;
     qs[1] = __shfl_sync(0xffffffffu, unit, 8 * t + 4) * p.scale_log2;

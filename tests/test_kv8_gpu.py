@@ -447,6 +447,48 @@ def test_attend_query_range(scale):
     check_attend(kv, cfg, 4, lists, q, o, lens)
 
 
+@pytest.mark.parametrize("code", CODES)
+def test_attend_largest_queries(code):
+    """Queries in bf16's last binade (2^127 and above), keys as much smaller."""
+    lens = [700]
+    cfg = sas.Config(4, 1, token_budget=512, attn_scale=2.0 ** -34)
+    kv = K.make_cache(1, 1, 11, code, False, lens, DEV, seed=9)
+    kv.k_scale.mul_(2.0 ** -97)
+    kv.k_tail.mul_(2.0 ** -97)
+    g = torch.Generator().manual_seed(1)
+    q = (1 + 0.98 * torch.rand((1, 4, 128), generator=g)) * 2.0 ** 127 * (torch.randint(0, 2, (1, 4, 128), generator=g) * 2 - 1)
+    ws = ws_for(cfg)
+    lists = random_lists(lens, 1, 8, 8)
+    q, o = run_attend(kv, cfg, 4, lists, ws, q=q.bfloat16().to(DEV))
+    assert ok(ws)
+    check_attend(kv, cfg, 4, lists, q, o, lens)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("out,drop", [("bf16", 23.4), ("f32", 20.4)])
+def test_attend_one_key_takes_the_weight(code, out, drop):
+    """One key `drop` powers of two above all others, its value zero: the output is the others' share alone."""
+    lens = [64 * 40]
+    cfg = sas.Config(2, 1, token_budget=4096, attn_scale=1.0, out_dtype=out)
+    kv = K.make_cache(1, 1, 40, code, False, lens, DEV, seed=9)
+    kv.k.view(torch.uint8).zero_()
+    kv.k[0, 0, 0] = torch.ones(128, device=DEV).to(code)
+    kv.k_scale.fill_(drop * math.log(2) / 128)
+    kv.k_tail.zero_()
+    # values in the 16 rows of each block that meet the large key's maximum first
+    v = (torch.rand((1, 1, 40, 64, 128), generator=torch.Generator().manual_seed(3)) * 100 + 20).to(code)
+    v.view(torch.uint8)[:, :, :, 16:] = 0
+    v.view(torch.uint8)[:, :, 0, 0] = 0
+    kv.v.copy_(v.view(1, 1, 2560, 128).to(DEV))
+    kv.v_tail[:, :, 16:] = 0
+    q = torch.ones(1, 2, 128, dtype=torch.bfloat16, device=DEV)
+    ws = ws_for(cfg)
+    lists = [[list(range(40))]]
+    q, o = run_attend(kv, cfg, 2, lists, ws, q=q)
+    assert ok(ws)
+    check_attend(kv, cfg, 2, lists, q, o, lens)
+
+
 def test_attend_rising_logits():
     """Logits that grow block by block by far more than the lazy maximum's step."""
     lens = [64 * 40]
