@@ -17,6 +17,7 @@ cudaError_t prepare_prefill_kernels();
 cudaError_t prepare_backward_kernels();
 cudaError_t prepare_prefill_backward_kernels();
 cudaError_t prepare_kv8_kernels();
+cudaError_t prepare_norm_rope_kernels();
 }
 
 namespace {
@@ -68,6 +69,7 @@ cudaError_t prepare() {
     if (e == cudaSuccess) e = sas::prepare_backward_kernels();
     if (e == cudaSuccess) e = sas::prepare_prefill_backward_kernels();
     if (e == cudaSuccess) e = sas::prepare_kv8_kernels();
+    if (e == cudaSuccess) e = sas::prepare_norm_rope_kernels();
     g_dev_err[dev] = e;
   });
   return g_dev_err[dev];
@@ -939,6 +941,7 @@ sas_status norm_rope_call(const sas_config* cfg, const sas_rows* dq_out, const s
     return st;
   if (!has_q && !has_k) return SAS_OK;
   if (cfg->num_q_heads + cfg->num_kv_heads > 65535) return SAS_ERR_UNSUPPORTED;
+  if (prepare() != cudaSuccess) return SAS_ERR_CUDA;
   sas::NormRopeParams p{};
   sas::fill_rope_table(p.rope, rope_base);
   p.batch = batch;

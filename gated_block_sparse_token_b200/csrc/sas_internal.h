@@ -414,22 +414,32 @@ struct NormRopeGrid {
   int x, chunk, q_chunks, k_chunks;
 };
 
-// Heads of a CTA: as many as leave two waves of resident CTAs (148 SMs x 4; the
-// gradient one wave of 148 x 2), so that the angles are shared by many heads of
-// a long batch while a decode step's few rows spread over the SMs.  A forward
-// CTA takes at most 16 (32,768 tokens: 8 heads 243 us, 16 heads 238, all 32
-// 254).  The gradient keeps at most kNrMaxCtas CTAs, which then walk the tokens.
+// Heads of a CTA: the angles of its tokens are shared by them, while a decode
+// step's few rows spread over the SMs.  Forward: up to 8, the number whose waves
+// of 148 x 4 resident CTAs, each 2.5 us and 0.4 a head, are done first (32 + 8
+// heads, by 1 / 2 / 3 / 4 / 5 / 8 heads a CTA: 1,021 tokens 10.4 / 8.0 / 7.6 / 8.4 /
+// 7.5 / 11.3 us, 4,096 tokens 33.4 / 22.7 / 19.2 / 18.0 / 17.3 / 18.7; 65,536 by 8 /
+// 16 / 32: 209.6 / 212.1 / 212.2).  Gradient: the fewest that fit 148 x 2 resident
+// CTAs, or all (3 x 700 tokens 15.1 us, with a few CTAs more than fit 17.8); at
+// most kNrMaxCtas CTAs, which then walk the tokens.
 inline NormRopeGrid norm_rope_grid(int batch, int tokens, int hq, int hkv, bool back) {
   const long long slots = (static_cast<long long>(batch) * tokens + kNrThreads / 8 - 1) / (kNrThreads / 8);
   const int most = std::max(std::max(hq, hkv), 1);
-  const long long want = slots * (hq + hkv) / (back ? 148 * 2 : 148 * 8);
+  const auto chunks = [](int heads, int c) { return (heads + c - 1) / c; };
   NormRopeGrid g{};
-  g.chunk = static_cast<int>(std::min<long long>(std::max<long long>(want, 1), back ? most : std::min(most, 16)));
-  for (;; ++g.chunk) {
-    g.q_chunks = (hq + g.chunk - 1) / g.chunk;
-    g.k_chunks = (hkv + g.chunk - 1) / g.chunk;
-    if (!back || g.q_chunks + g.k_chunks <= kNrMaxCtas || g.chunk >= most) break;
+  g.chunk = 1;
+  if (back) {
+    while (g.chunk < most && (chunks(hq, g.chunk) + chunks(hkv, g.chunk)) * slots > 148 * 2) ++g.chunk;
+  } else {
+    long long best = 0;
+    for (int c = 1; c <= std::min(most, 8); ++c) {
+      const long long waves = ((chunks(hq, c) + chunks(hkv, c)) * slots + 148 * 4 - 1) / (148 * 4);
+      const long long cost = waves * (25 + 4 * c);
+      if (c == 1 || cost < best) best = cost, g.chunk = c;
+    }
   }
+  g.q_chunks = chunks(hq, g.chunk);
+  g.k_chunks = chunks(hkv, g.chunk);
   g.x = static_cast<int>(slots);
   if (back) g.x = static_cast<int>(std::min<long long>(slots, std::max(kNrMaxCtas / (g.q_chunks + g.k_chunks), 1)));
   return g;

@@ -319,9 +319,9 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 // sequences fill the SMs; a second kernel merges the chunks' partial sums (16
 // pairs x 2,000 blocks: 92-101 us; clusters of 8 114-121, of 16, which not every
 // GPC holds twice, 105-118).
-// Measured: 64 pairs x 32 blocks 11.6 us (2.9 TB/s; the launch, the chain of
+// Measured: 64 pairs x 32 blocks 10.9 us (3.1 TB/s; the launch, the chain of
 // length, list, table and first tile, and the merge are half of it), 256 pairs x
-// 64 blocks 53 us (5.1 TB/s), 128 pairs x 500 blocks dense 172 us (6.0 TB/s).
+// 64 blocks 54 us (5.0 TB/s), 128 pairs x 500 blocks dense 172 us (6.0 TB/s).
 constexpr int kKaStages = 3;                // ring slots of a warp
 constexpr int kKaSlot = 2 * 16 * kDim;      // 16 rows of K, then of V
 constexpr int kKaHeadPair = 2 * kDim + 4;   // floats between head pairs of a partial (bank spread)
@@ -404,12 +404,6 @@ struct KaQuery<kCodeE4m3, F32OUT> {  // f16; k-step j: b[2j], b[2j + 1]
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
   return r;
 }
 

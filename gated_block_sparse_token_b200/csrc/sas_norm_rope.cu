@@ -16,9 +16,9 @@
 // keeps its token's 8 (cos, sin) pairs in registers over a chunk of heads:
 // the angles are reduced in double precision (exact for any int32 position)
 // and would otherwise cost more than the row.  Measured, bf16, 32 + 8 heads:
-// 2 x 32,768 tokens 227 us (5.9 TB/s), one decode step of 8 sequences 2.5 us;
-// gradient of 8 x 1,021 padded tokens of 40 + 8 heads 45 us (5.0 TB/s) and 3 for
-// the gains' sum.
+// 2 x 32,768 tokens 210 us (6.4 TB/s), one decode step of 8 sequences 2.5 us;
+// gradient of 8 x 1,021 padded tokens of 40 + 8 heads 36 us (6.2 TB/s) and 3 for
+// the gains' sum, of 2 x 32,768 tokens 302 (6.0 TB/s).
 #include "sas_internal.h"
 
 namespace sas {
@@ -32,6 +32,10 @@ template <typename T>
 struct Raw8 {
   uint4 r[sizeof(T) / 2];
 };
+// the ring of the next heads: slots, and bytes of one (16-byte pieces of x, and of dy, a thread)
+constexpr int kNrStages = 4;
+__host__ __device__ constexpr int nr_stage(bool back) { return (back ? 4 : 2) * 16 * kNrThreads; }
+
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, Raw8<T>& x) {
 #pragma unroll
@@ -67,7 +71,7 @@ __device__ __forceinline__ float sum8lanes(float v) {
 
 // blockIdx.y: a chunk of p.chunk heads, the query heads' chunks first (a
 // chunk never mixes queries and keys); blockIdx.x: tokens, 32 at a time.
-template <typename T, bool kBack>
+template <typename T, bool kBack, bool kRing>
 __global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4)
     norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   griddep_launch_dependents();
@@ -88,6 +92,10 @@ __global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4)
 #pragma unroll
   for (int e = 0; e < 8; ++e) alo[e] = ahi[e] = 0.f;
 
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  static_assert(!kRing || sizeof(T) == 2, "one 16-byte piece is eight elements");
+  const uint32_t ring = kRing ? smem_u32(smem_raw) + 16 * tid : 0u;
+
   const int n_tok = p.batch * p.tokens;
   for (int n0 = static_cast<int>(blockIdx.x) * kNrRowsPerCta; n0 < n_tok;
        n0 += static_cast<int>(gridDim.x) * kNrRowsPerCta) {
@@ -101,12 +109,28 @@ __global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4)
            static_cast<long long>(t) * yv.token + 8 * j;
     const T* dy = static_cast<const T*>(dv.data) + static_cast<long long>(s) * dv.seq +
                   static_cast<long long>(t) * dv.token + 8 * j;
-    // the next head's loads go out before this one's store, which the compiler
-    // could not arrange: the output may be the input.  (Two and four heads ahead
-    // cost the forward its fourth CTA an SM: 254 and 283 us against 238 for
-    // 2 x 32,768 tokens of 32 + 8 heads.)
+    // The next heads' loads go out before this one's store, which the compiler
+    // could not arrange: the output may be the input.  bf16: every lane copies its
+    // pieces of the next three heads to its own places in shared memory; an SM's
+    // registers hold one head ahead (2 x 32,768 tokens of 32 + 8 heads 212 against
+    // 228 us, the gradient of 8 x 1,021 of 40 + 8 42 against 50).  An fp32 lane's
+    // pieces are every other 16 bytes, half sectors to such a copy: through
+    // registers (gradient 84 us against 138), as is a single head (a decode step:
+    // 2.5 us against 2.6).
     Raw8<T> bx[2], bd[2];
+    const auto slot = [&](int h) { return ring + static_cast<uint32_t>(h - h0) % kNrStages * nr_stage(kBack); };
     auto fetch = [&](int h) {
+      if constexpr (kRing) {
+        const uint8_t* sx = reinterpret_cast<const uint8_t*>(x + h * xv.head);
+        const uint8_t* sd = reinterpret_cast<const uint8_t*>(dy + h * dv.head);
+        cp_async16(slot(h), sx);
+        cp_async16(slot(h) + 16 * kNrThreads, sx + 128);
+        if constexpr (kBack) {
+          cp_async16(slot(h) + 32 * kNrThreads, sd);
+          cp_async16(slot(h) + 48 * kNrThreads, sd + 128);
+        }
+        return;
+      }
       load8(x + h * xv.head, bx[0]);
       load8(x + h * xv.head + 64, bx[1]);
       if constexpr (kBack) {
@@ -115,11 +139,32 @@ __global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4)
       }
     };
     bx[0] = bx[1] = bd[0] = bd[1] = Raw8<T>{};
-    if (live) fetch(h0);
+    if constexpr (kRing) {
+#pragma unroll
+      for (int i = 0; i < kNrStages - 1; ++i) {
+        if (live && h0 + i < h1) fetch(h0 + i);
+        cp_async_commit();
+      }
+    } else {
+      if (live) fetch(h0);
+    }
     float cs[8], sn[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) rope_cos_sin(p.rope.theta_over_pi[8 * j + e], max(pos, 0), cs[e], sn[e]);
     for (int h = h0; h < h1; ++h) {
+      if constexpr (kRing) {
+        cp_async_wait<kNrStages - 2>();
+        if (live) {
+          bx[0].r[0] = lds128(slot(h));
+          bx[1].r[0] = lds128(slot(h) + 16 * kNrThreads);
+          if constexpr (kBack) {
+            bd[0].r[0] = lds128(slot(h) + 32 * kNrThreads);
+            bd[1].r[0] = lds128(slot(h) + 48 * kNrThreads);
+          }
+        }
+        if (live && h + kNrStages - 1 < h1) fetch(h + kNrStages - 1);  // into the place of the head before
+        cp_async_commit();
+      }
       float lo[8], hi[8];
       unpack8(bx[0], lo);
       unpack8(bx[1], hi);
@@ -127,7 +172,7 @@ __global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4)
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], ss));
       if constexpr (!kBack) {
-        if (live && h + 1 < h1) fetch(h + 1);
+        if (!kRing && live && h + 1 < h1) fetch(h + 1);
         const float r = rsqrtf(sum8lanes(ss) * (1.f / kDim) + p.eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -139,7 +184,7 @@ __global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4)
         float dlo[8], dhi[8];
         unpack8(bd[0], dlo);
         unpack8(bd[1], dhi);
-        if (live && h + 1 < h1) fetch(h + 1);
+        if (!kRing && live && h + 1 < h1) fetch(h + 1);
         const float r = rsqrtf(sum8lanes(ss) * (1.f / kDim) + p.eps);
         float dot = 0.f;
 #pragma unroll
@@ -227,18 +272,26 @@ cudaError_t launch_norm_rope(bool f32, bool back, NormRopeParams p, float* dgamm
   p.chunk = g.chunk;
   p.q_chunks = g.q_chunks;
   const dim3 grid(static_cast<unsigned>(g.x), static_cast<unsigned>(g.q_chunks + g.k_chunks));
-  cudaError_t e;
-  if (!back) {
-    return f32 ? launch_pdl(norm_rope_kernel<float, false>, grid, kNrThreads, 0, stream, 0, p)
-               : launch_pdl(norm_rope_kernel<__nv_bfloat16, false>, grid, kNrThreads, 0, stream, 0, p);
-  }
-  e = f32 ? launch_pdl(norm_rope_kernel<float, true>, grid, kNrThreads, 0, stream, 0, p)
-          : launch_pdl(norm_rope_kernel<__nv_bfloat16, true>, grid, kNrThreads, 0, stream, 0, p);
+  const bool ring = !f32 && g.chunk > 1;
+  const size_t smem = ring ? kNrStages * nr_stage(back) : 0;
+  const auto go = [&](auto* kernel) { return launch_pdl(kernel, grid, kNrThreads, smem, stream, 0, p); };
+  if (!back)
+    return f32 ? go(norm_rope_kernel<float, false, false>)
+               : (ring ? go(norm_rope_kernel<__nv_bfloat16, false, true>)
+                       : go(norm_rope_kernel<__nv_bfloat16, false, false>));
+  const cudaError_t e = f32 ? go(norm_rope_kernel<float, true, false>)
+                            : (ring ? go(norm_rope_kernel<__nv_bfloat16, true, true>)
+                                    : go(norm_rope_kernel<__nv_bfloat16, true, false>));
   if (e != cudaSuccess) return e;
   int q_rows = g.q_chunks * g.x, k_rows = g.k_chunks * g.x;
   if (dgamma_q == dgamma_k && p.hq > 0 && p.hkv > 0) q_rows += k_rows, k_rows = 0;  // one gain: one sum
   return launch_pdl(norm_rope_gain_kernel, dim3(kDim / 32, 2), 1024, 0, stream, 0, p.ws_part, q_rows, k_rows, dgamma_q,
                     dgamma_k);
+}
+
+cudaError_t prepare_norm_rope_kernels() {
+  return cudaFuncSetAttribute(norm_rope_kernel<__nv_bfloat16, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kNrStages * nr_stage(true));
 }
 
 }  // namespace sas
