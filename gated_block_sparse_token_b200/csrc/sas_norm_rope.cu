@@ -185,7 +185,10 @@ __global__ void __launch_bounds__(kNrThreads, kBack ? 2 : 4)
         unpack8(bd[0], dlo);
         unpack8(bd[1], dhi);
         if (!kRing && live && h + 1 < h1) fetch(h + 1);
-        const float r = rsqrtf(sum8lanes(ss) * (1.f / kDim) + p.eps);
+        // a row that is not live is zeros here: r 0 keeps it out of the gains' sums
+        // also where eps is 0 and 1 / sqrt(mean + eps) infinite
+        const float inv = rsqrtf(sum8lanes(ss) * (1.f / kDim) + p.eps);
+        const float r = live ? inv : 0.f;
         float dot = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
