@@ -295,10 +295,12 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 //                common to p and its sum cancels), so most blocks need one vote
 //                and no shuffles;
 //   O^T += V^T P^T  m16n8k16 f16 (codes are exact in f16), the P fragment
-//                transposed in place by movmatrix.  P is rounded to f16 (before a
-//                bf16 output); for an fp32 output a second product carries the
-//                remainder.  It enters as 2^kKaShift p, so that the rounding is
-//                2^-11 relative for every key down to 2^-25 of the largest: a few
+//                transposed in place by movmatrix.  P enters as two f16 terms, in
+//                two products: 2^-22 of it.  (One term, 2^-11, left a few in a
+//                hundred bf16 outputs on the other side of a rounding border; it
+//                saves 2.5 of 96 us over 2 x 128k tokens, 0.5 of 11.5 on 64 pairs x
+//                32 blocks.)  It enters as 2^kKaShift p, so that this holds for every
+//                key down to 2^-14 of the largest, and 2^-15 down to 2^-21: a few
 //                keys that take nearly all the weight leave the others exact
 //                enough (unshifted, a hundred thousand keys at 2^-24 were a third
 //                off).  V's scale takes the factor back.  The sum of P runs over
@@ -309,8 +311,8 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 // g) of its eight: with the swizzle both operands' loads are then free of bank
 // conflicts.  The block's two scales enter as fp32 factors of S and O.
 // The current block comes from the bf16 tail on bf16 products (P as a sum of
-// two bf16 terms, three for an fp32 output), rows past the length masked, while
-// the ring first fills.
+// three bf16 terms, 2^-24 of it), rows past the length masked, while the ring
+// first fills.
 //
 // Two ways to divide the work.  Lists (and dense attention without the
 // workspace for the other way): a cluster of CTAs a pair, which merge through
@@ -448,9 +450,9 @@ __device__ __forceinline__ void raise_max(KaState& st, const float (&sc)[4]) {
 // memory, swizzled in 16-byte units by their row modulo 8.  kr: the K row of
 // this lane (key g), vr: the V rows of keys 2t and 2t + 1 (row 8 further: keys
 // g + 8, ...).
-template <int CODE, bool SPLIT>
+template <int CODE, bool F32OUT>
 __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint32_t vs_addr,
-                                             const KaQuery<CODE, SPLIT>& q, const float (&qs)[2], float ks, float vs) {
+                                             const KaQuery<CODE, F32OUT>& q, const float (&qs)[2], float ks, float vs) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int kr = (2 * (g >> 1) + (g >> 2)) ^ (4 * (g & 1)), vr = 2 * t + (t >> 1);
   uint4 x[4];
@@ -464,7 +466,7 @@ __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint
   const uint4 y0 = lds128(at0), y1 = lds128(at1), y2 = lds128(at0 + 8 * kDim), y3 = lds128(at1 + 8 * kDim);
   float sc[4];
   if constexpr (CODE == kCodeInt8) {
-    constexpr int N = KaQuery<CODE, SPLIT>::kDigits;
+    constexpr int N = KaQuery<CODE, F32OUT>::kDigits;
     int d[2][N][4] = {};  // independent chains of two products
 #pragma unroll
     for (int c = 0; c < 2; ++c)
@@ -525,24 +527,20 @@ __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint
   st.l[1] = fmaf(p[1] + p[3], kKaUnshift, st.l[1]);
   const uint32_t h0 = pack_f16x2(p[0], p[1]), h1 = pack_f16x2(p[2], p[3]);
   const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
-  uint32_t e0 = 0, e1 = 0;
-  if constexpr (SPLIT) {
-    e0 = transpose8x8(pack_f16x2(p[0] - f16_lo(h0), p[1] - f16_hi(h0)));
-    e1 = transpose8x8(pack_f16x2(p[2] - f16_lo(h1), p[3] - f16_hi(h1)));
-  }
+  const uint32_t e0 = transpose8x8(pack_f16x2(p[0] - f16_lo(h0), p[1] - f16_hi(h0)));
+  const uint32_t e1 = transpose8x8(pack_f16x2(p[2] - f16_lo(h1), p[3] - f16_hi(h1)));
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     float o[4] = {0.f, 0.f, 0.f, 0.f};
     mma_f16(o, a[j][0], a[j][1], a[j][2], a[j][3], b0, b1);
-    if constexpr (SPLIT) mma_f16(o, a[j][0], a[j][1], a[j][2], a[j][3], e0, e1);
+    mma_f16(o, a[j][0], a[j][1], a[j][2], a[j][3], e0, e1);
 #pragma unroll
     for (int e = 0; e < 4; ++e) st.acc[j][e] = fmaf(o[e], vs, st.acc[j][e]);
   }
 }
 
 // One 16-key slice of the current block, from the bf16 tail: rows
-// row0 .. row0 + 15 of which those below `rows` count.  P as TERMS bf16 terms.
-template <int TERMS>
+// row0 .. row0 + 15 of which those below `rows` count.
 __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt, const __nv_bfloat16* vt,
                                             const __nv_bfloat16* q, bool head_ok, int row0, int rows, float scale) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -570,9 +568,10 @@ __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt
   for (int e = 0; e < 4; ++e) p[e] = (e < 2 ? in0 : in1) ? exp2_approx(sc[e] - (st.m[e & 1] + kKaShift)) : 0.f;
   st.l[0] += p[0] + p[2];
   st.l[1] += p[1] + p[3];
-  uint32_t b[TERMS][2];
+  constexpr int kTerms = 3;  // of P
+  uint32_t b[kTerms][2];
 #pragma unroll
-  for (int n = 0; n < TERMS; ++n) {
+  for (int n = 0; n < kTerms; ++n) {
     const uint32_t h0 = pack_bf16x2(p[0], p[1]), h1 = pack_bf16x2(p[2], p[3]);
     b[n][0] = transpose8x8(h0);
     b[n][1] = transpose8x8(h1);
@@ -595,7 +594,7 @@ __device__ __forceinline__ void attend_tail(KaState& st, const __nv_bfloat16* kt
     const uint32_t a0 = __byte_perm(v[0][w], v[1][w], sel), a1 = __byte_perm(v[0][4 + w], v[1][4 + w], sel);
     const uint32_t a2 = __byte_perm(v[2][w], v[3][w], sel), a3 = __byte_perm(v[2][4 + w], v[3][4 + w], sel);
 #pragma unroll
-    for (int n = 0; n < TERMS; ++n) mma_bf16_16816(st.acc[j], a0, a1, a2, a3, b[n][0], b[n][1]);
+    for (int n = 0; n < kTerms; ++n) mma_bf16_16816(st.acc[j], a0, a1, a2, a3, b[n][0], b[n][1]);
   }
 }
 
@@ -824,8 +823,7 @@ __global__ void __launch_bounds__(32 * kKaWarps, 2)
   const bool tail_turn = CHUNKS ? (ch.q == ch.chunks - 1 && grp == 0) : grp == (m - 1) % js;
   if (!bad && tail_turn && 16 * quarter < L - c * kBlock) {
     const size_t off = static_cast<size_t>(pair) * (kBlock * kDim);
-    attend_tail<F32OUT ? 3 : 2>(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * quarter, L - c * kBlock,
-                                p.scale_log2);
+    attend_tail(st, p.kv.k_tail + off, p.kv.v_tail + off, qrow, g < G, 16 * quarter, L - c * kBlock, p.scale_log2);
   }
 
   // ---- the stored blocks

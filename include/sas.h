@@ -620,10 +620,9 @@ SAS_API size_t sas_sparse_decode_kv8_workspace_bytes(const sas_config* cfg, int3
  *        block is cut into equal chunks that a second kernel merges (calls that
  *        may overlap on the GPU then need a workspace each)
  * Logits, softmax statistics and sums are fp32.  The probabilities enter the
- * product with the values as f16 (bf16 output: 2^-11 of each down to 2^-25 of
- * the largest) or as a sum of two f16 terms (fp32 output: 2^-15 of each down to
- * 2^-21 of the largest), over the tail as sums of two and three bf16 terms.  kv_dtype
- * must be bf16; the gated mode is refused as by sas_sparse_decode.
+ * product with the values as sums of two f16 terms (2^-22 of each down to 2^-14
+ * of the largest, 2^-15 down to 2^-21), over the tail of three bf16 terms.
+ * kv_dtype must be bf16; the gated mode is refused as by sas_sparse_decode.
  */
 SAS_API sas_status sas_sparse_decode_kv8(const sas_config* cfg, const void* q, const sas_kv8* kv,
                                          const int32_t* sel_idx, const int32_t* sel_count,

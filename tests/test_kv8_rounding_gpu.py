@@ -1,0 +1,44 @@
+"""How exact the 8-bit decode attention is, on inputs where a coarser arithmetic
+shows."""
+import pytest
+import torch
+
+from gated_block_sparse_token_b200 import sas
+
+import kv8_testlib as K
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def attend(kv, hq, q, out, ws, lists=None, **cfg):
+    """sparse_decode_kv8 over every block, or the first len(lists[s]) entries of a list per sequence (one KV head)."""
+    cfg = sas.Config(hq, 1, out_dtype=out, **cfg)
+    o = torch.full((kv.batch, hq, 128), float("nan"), dtype=sas.out_dtype(cfg), device=DEV)
+    sel = cnt = None
+    if lists is not None:
+        sel = torch.full((kv.batch, 1, cfg.max_sel), -7, dtype=torch.int32, device=DEV)
+        for s, blocks in enumerate(lists):
+            sel[s, 0, :len(blocks)] = torch.tensor(blocks, dtype=torch.int32)
+        cnt = torch.tensor([[len(b)] for b in lists], dtype=torch.int32, device=DEV)
+    sas.sparse_decode_kv8(cfg, q.to(DEV), kv, sel, cnt, o, ws)
+    torch.cuda.synchronize()
+    assert sas.get_device_status(ws) == sas.SAS_OK
+    return o
+
+
+@pytest.mark.parametrize("code", [K.E4M3])
+@pytest.mark.parametrize("chunks", [False, True])
+@pytest.mark.parametrize("listed", [False, True])
+def test_bf16_output_is_the_fp32_one_rounded(code, chunks, listed):
+    """One arithmetic for both outputs: the bf16 output is the fp32 output rounded once, bit for bit."""
+    lens = [64 * 90 + 17, 5, 64 * 70, 2049]
+    kv = K.make_cache(4, 1, 91, code, True, lens, DEV, seed=17)
+    cfg = sas.Config(8, 1)
+    n = sas.sparse_decode_kv8_workspace_bytes(cfg, 4) if chunks else 256
+    ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    q = torch.randn(4, 8, 128, generator=torch.Generator().manual_seed(5)).bfloat16()
+    lists = [[b for b in range(0, (L - 1) // 64, 3)][:31] + [(L - 1) // 64] for L in lens] if listed else None
+    a = attend(kv, 8, q, "f32", ws, lists)
+    b = attend(kv, 8, q, "bf16", ws, lists)
+    assert torch.equal(a.bfloat16(), b)
