@@ -281,10 +281,13 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 // two copies a block: 59; this one 53.)
 //   S^T = K q^T  the 16 keys are the rows, the (up to 8) heads of the group the
 //                columns.  int8: m16n8k32 on the codes as they are stored, the
-//                query as the signed 8-bit digits of a fixed-point number per
-//                head: two digits, 2^-16 of the head's largest value (its bf16
-//                values carry 2^-8 of their own), for a bf16 output, three, 2^-23,
-//                for fp32; its sums are exact.  e4m3: m16n8k16 f16, the codes
+//                query as the three signed 8-bit digits of a fixed-point number
+//                per head, in steps of 2^-21 of the power of two below the head's
+//                largest value: its bf16 values stay exact down to 2^-14 of that,
+//                and within 2^-22 of it below; its sums are exact.  (Two digits,
+//                steps of 2^-14, cost the small channels beside a dominant one
+//                their value; they save 0.9 of 13.5 us on 64 pairs x 32 blocks, 0.4
+//                of 97 over 2 x 128k tokens.)  e4m3: m16n8k16 f16, the codes
 //                converted (exact), the query scaled by a power of two per head
 //                into f16's range (its bf16 values stay exact down to 2^-15 of the
 //                largest, and off by 2^-25 of it below).  (The e4m3 form of
@@ -361,17 +364,17 @@ __device__ __forceinline__ float pow2_down(uint32_t e) {  // 2^(127 - e), e = 25
   return __uint_as_float(e < 254u ? (254u - e) << 23 : 0x00400000u);
 }
 
-template <int CODE, bool F32OUT>
+template <int CODE>
 struct KaQuery {  // int8: sum_n 256^n digit_n; k-step j: b[.][2j], b[.][2j + 1]
-  static constexpr int kDigits = F32OUT ? 3 : 2;
+  static constexpr int kDigits = 3;
   uint32_t b[kDigits][8];
 
   __device__ __forceinline__ float set(const uint32_t (&raw)[16], uint32_t e) {
-    // largest value to below 127/128 of 2^15 (two digits) or 2^22 (three, the most
-    // that `magic` leaves room for): every digit is a signed byte
-    constexpr float top = (kDigits == 2 ? 16384.f : 2097152.f) * (127.f / 128.f);
+    // largest value to below 2^22, the most that `magic` leaves room for, and a bit
+    // less than three signed bytes hold
+    constexpr float top = 2097152.f;
     constexpr float magic = 12582912.f;  // 1.5 * 2^23: its sum holds the rounded value in the low bits
-    constexpr uint32_t bias = kDigits == 2 ? 0x8080u : 0x808080u;
+    constexpr uint32_t bias = 0x808080u;
     const float dn = pow2_down(e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -391,8 +394,8 @@ struct KaQuery {  // int8: sum_n 256^n digit_n; k-step j: b[.][2j], b[.][2j + 1]
     return __uint_as_float(e << 23) * (1.f / top);
   }
 };
-template <bool F32OUT>
-struct KaQuery<kCodeE4m3, F32OUT> {  // f16; k-step j: b[2j], b[2j + 1]
+template <>
+struct KaQuery<kCodeE4m3> {  // f16; k-step j: b[2j], b[2j + 1]
   uint32_t b[16];
 
   __device__ __forceinline__ float set(const uint32_t (&raw)[16], uint32_t e) {
@@ -450,9 +453,9 @@ __device__ __forceinline__ void raise_max(KaState& st, const float (&sc)[4]) {
 // memory, swizzled in 16-byte units by their row modulo 8.  kr: the K row of
 // this lane (key g), vr: the V rows of keys 2t and 2t + 1 (row 8 further: keys
 // g + 8, ...).
-template <int CODE, bool F32OUT>
-__device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint32_t vs_addr,
-                                             const KaQuery<CODE, F32OUT>& q, const float (&qs)[2], float ks, float vs) {
+template <int CODE>
+__device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint32_t vs_addr, const KaQuery<CODE>& q,
+                                             const float (&qs)[2], float ks, float vs) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int kr = (2 * (g >> 1) + (g >> 2)) ^ (4 * (g & 1)), vr = 2 * t + (t >> 1);
   uint4 x[4];
@@ -466,7 +469,7 @@ __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint
   const uint4 y0 = lds128(at0), y1 = lds128(at1), y2 = lds128(at0 + 8 * kDim), y3 = lds128(at1 + 8 * kDim);
   float sc[4];
   if constexpr (CODE == kCodeInt8) {
-    constexpr int N = KaQuery<CODE, F32OUT>::kDigits;
+    constexpr int N = KaQuery<CODE>::kDigits;
     int d[2][N][4] = {};  // independent chains of two products
 #pragma unroll
     for (int c = 0; c < 2; ++c)
@@ -478,7 +481,7 @@ __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       sc[e] = fmaf(static_cast<float>(d[0][1][e] + d[1][1][e]), 256.f, static_cast<float>(d[0][0][e] + d[1][0][e]));
-      if constexpr (N == 3) sc[e] = fmaf(static_cast<float>(d[0][N - 1][e] + d[1][N - 1][e]), 65536.f, sc[e]);
+      sc[e] = fmaf(static_cast<float>(d[0][2][e] + d[1][2][e]), 65536.f, sc[e]);
     }
   } else {
     float d[2][4] = {};  // two chains of products
@@ -789,7 +792,7 @@ __global__ void __launch_bounds__(32 * kKaWarps, 2)
   }
 
   // ---- the query, as B fragments: head g, dims 16t .. and 64 + 16t ..
-  KaQuery<CODE, F32OUT> qf;
+  KaQuery<CODE> qf;
   float qs[2];
   {
     uint32_t mag = 0;
@@ -835,8 +838,8 @@ __global__ void __launch_bounds__(32 * kKaWarps, 2)
     }
     cp_async_wait<kKaStages - 1>();
     __syncwarp();
-    attend_codes<CODE, F32OUT>(st, slot, slot + 16 * kDim, qf, qs, __shfl_sync(0xffffffffu, ks_c, i & 31),
-                               __shfl_sync(0xffffffffu, vs_c, i & 31));
+    attend_codes<CODE>(st, slot, slot + 16 * kDim, qf, qs, __shfl_sync(0xffffffffu, ks_c, i & 31),
+                       __shfl_sync(0xffffffffu, vs_c, i & 31));
     __syncwarp();
     const int nxt = i + kKaStages;  // into the slot just used
     const int tile = __shfl_sync(0xffffffffu, ((i ^ nxt) & ~31) ? tile_n : tile_c, nxt & 31);

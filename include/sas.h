@@ -619,9 +619,11 @@ SAS_API size_t sas_sparse_decode_kv8_workspace_bytes(const sas_config* cfg, int3
  *        sas_sparse_decode_kv8_workspace_bytes(cfg, B), attention over every
  *        block is cut into equal chunks that a second kernel merges (calls that
  *        may overlap on the GPU then need a workspace each)
- * Logits, softmax statistics and sums are fp32.  The probabilities enter the
- * product with the values as sums of two f16 terms (2^-22 of each down to 2^-14
- * of the largest, 2^-15 down to 2^-21), over the tail of three bf16 terms.
+ * Logits, softmax statistics and sums are fp32.  Over the stored blocks the query
+ * is exact down to 2^-14 of the power of two below its head's largest value, and
+ * within 2^-22 of that below.  The probabilities enter the product with the values
+ * as sums of two f16 terms (2^-22 of each down to 2^-14 of the largest, 2^-15 down
+ * to 2^-21), over the tail of three bf16 terms.
  * kv_dtype must be bf16; the gated mode is refused as by sas_sparse_decode.
  */
 SAS_API sas_status sas_sparse_decode_kv8(const sas_config* cfg, const void* q, const sas_kv8* kv,

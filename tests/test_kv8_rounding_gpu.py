@@ -5,10 +5,12 @@ import torch
 
 from gated_block_sparse_token_b200 import sas
 
+import kv8_bounds as N
 import kv8_testlib as K
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+CODES = [K.E4M3, K.INT8]
 
 
 def attend(kv, hq, q, out, ws, lists=None, **cfg):
@@ -27,7 +29,7 @@ def attend(kv, hq, q, out, ws, lists=None, **cfg):
     return o
 
 
-@pytest.mark.parametrize("code", [K.E4M3])
+@pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("chunks", [False, True])
 @pytest.mark.parametrize("listed", [False, True])
 def test_bf16_output_is_the_fp32_one_rounded(code, chunks, listed):
@@ -42,3 +44,28 @@ def test_bf16_output_is_the_fp32_one_rounded(code, chunks, listed):
     a = attend(kv, 8, q, "f32", ws, lists)
     b = attend(kv, 8, q, "bf16", ws, lists)
     assert torch.equal(a.bfloat16(), b)
+
+
+def check(inputs, code, out):
+    kv, q, scale = inputs
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    o = attend(kv, 8, q, out, ws, attn_scale=scale).cpu().double()
+    for s, qh, k, v, tail in N.heads(kv, q):
+        want, tol = N.tolerance(qh, k, v, tail, scale, code, out)
+        err = (o[s] - want).abs()
+        assert bool((err <= tol).all()), (s, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("peak", [64.0, 300.0])
+def test_dominant_query_channel(code, out, peak):
+    """The other channels keep their bf16 values."""
+    check(N.outlier(code, peak, DEV), code, out)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("stored", [False, True])
+def test_terms_of_p(code, stored):
+    """Exact logits: what the terms of P leave is all there is."""
+    check(N.one_channel(code, stored, DEV), code, "f32")
