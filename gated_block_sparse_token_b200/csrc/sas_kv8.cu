@@ -58,10 +58,10 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const __grid_constan
   const int L = p.kv.seq_lens[s];
   const int n = p.new_lens != nullptr ? p.new_lens[s] : p.max_new;
   const long long start = p.new_starts != nullptr ? p.new_starts[s] : 0;
-  const int L0 = L - n;
-  bool err = n < 0 || n > p.max_new || L0 < 0 || start < 0 || start + n > p.new_tokens ||
+  bool err = n < 0 || n > p.max_new || L < n || start < 0 || start + n > p.new_tokens ||
              static_cast<long long>(L) > static_cast<long long>(p.kv.blocks) * kBlock;
   if (!err && n == 0) return;  // uniform over the CTA, like every branch on n and L
+  const int L0 = err ? 0 : L - n;
   const int b_first = err ? 0 : L0 / kBlock, b_done = err ? 0 : L / kBlock;  // completed: [b_first, b_done)
   const RowsView src = half == 0 ? p.k_new : p.v_new;
   __nv_bfloat16* tail = const_cast<__nv_bfloat16*>(half == 0 ? p.kv.k_tail : p.kv.v_tail) +
