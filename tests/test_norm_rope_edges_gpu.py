@@ -1,5 +1,6 @@
-"""sas_qk_norm_rope and its gradient where rows contribute nothing: norm_eps 0
-with rows that are padded or lie behind the last token.
+"""sas_qk_norm_rope and its gradient where rows contribute nothing (norm_eps 0
+with rows that are padded or lie behind the last token; outputs of padded rows),
+and the gradient's walk over more tokens than its grid holds.
 
 Tolerances: those of the same sums in the other norm tests -- one rounding of
 the output's type, 2^-18 of the terms' magnitudes in dx, 2^-17 of the sum of
@@ -59,3 +60,53 @@ def test_gradient_without_eps(dt, B, T, hq, hkv, pad):
         pos[:, T - T // 3:] = -1
         pos[0, 0] = -5
     check_gradient(two, gradient(two, pos, 1e4, 0.0, dt), pos, 1e4, 0.0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,hq,hkv", [(1, 40_003, 4, 2), (3, 6_700, 2, 1)])
+def test_gradient_walks_over_tokens(dt, B, T, hq, hkv):
+    """More than 592 x 32 tokens: a CTA takes several groups of them, whose padding differs from one to the next."""
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    two = sides(B, T, hq, hkv, dtype, 13)
+    pos = torch.arange(B * T, dtype=torch.int32).view(B, T)
+    g = torch.Generator().manual_seed(5)
+    pos[torch.rand((B, T), generator=g) < 0.2] = -1
+    pos[:, T // 2:T // 2 + 3000] = -1                              # whole groups without a live row
+    got = gradient(two, pos, 1e6, 1e-6, dt)
+    check_gradient(two, got, pos, 1e6, 1e-6)
+    for a, b in zip(got, gradient(two, pos, 1e6, 1e-6, dt)):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,hq,hkv", [(5, 1, 8, 2), (2, 77, 1, 1), (3, 500, 32, 8)])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_padded_rows_keep_their_output(dt, B, T, hq, hkv, eps):
+    """Forward: a row with a negative position leaves its output as it was, into another tensor and in place, whatever
+    its input holds."""
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    (q, gq, _), (k, gk, _) = sides(B, T, hq, hkv, dtype, 17)
+    g = torch.Generator().manual_seed(6)
+    pos = torch.arange(B * T, dtype=torch.int32).view(B, T)
+    pad = torch.rand((B, T), generator=g) < 0.4
+    pad[0, 0] = True
+    pos[pad] = -1 - pos[pad]
+    live = ~pad[:, None, :, None]
+    for x in (q, k):
+        x.masked_fill_(~live.to(DEV), float("nan"))
+        x[0, :, 0] = 0
+    cfg = sas.Config(hq, hkv, kv_dtype=dt, norm_eps=eps)
+    qo, ko = torch.full_like(q, 5.0), torch.full_like(k, 5.0)
+    sas.qk_norm_rope(cfg, q, k, gq, gk, qo, ko, 1e5, positions=pos.to(DEV))
+    half = torch.finfo(dtype).eps / 2
+    for x, gamma, y in ((q, gq, qo), (k, gk, ko)):
+        want, size = K.norm_rope(x.cpu().nan_to_num(1.0), gamma.cpu(), pos.clamp_min(0), 1e5, eps)
+        y = y.cpu().double()
+        err = torch.where(live, (y - want).abs() - half * want.abs() - 2.0 ** -19 * size, -1.0)
+        assert bool((err <= 0).all()) and bool((torch.where(live, 5.0, y) == 5.0).all())
+    q0, k0 = q.clone(), k.clone()
+    sas.qk_norm_rope(cfg, q, k, gq, gk, q, k, 1e5, positions=pos.to(DEV))
+    torch.cuda.synchronize()
+    for x, x0, y in ((q, q0, qo), (k, k0, ko)):
+        bits = torch.int16 if dtype == torch.bfloat16 else torch.int32
+        assert torch.equal(x.view(bits), torch.where(live.to(DEV), y, x0).view(bits))
