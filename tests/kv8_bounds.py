@@ -27,11 +27,12 @@ def largest_power(q):
     return torch.exp2(torch.floor(torch.log2(q.abs().amax(-1, keepdim=True).clamp_min(2.0 ** -126))))
 
 
-def tolerance(q, k, v, tail, scale, code, out):
+def tolerance(q, k, v, tail, scale, code, out, times=None):
     """(out, tolerance) [G][128] of q [G][128] over keys k and values v [n][128], the last `tail` of them from the
-    tail; all float64."""
+    tail, key j counted times[j] times (default 1); all float64."""
     n = k.shape[0]
     stored = (torch.arange(n) < n - tail).double()
+    times = torch.ones(n, dtype=torch.float64) if times is None else times
     E = largest_power(q)
     logit = q @ k.T * scale
     dq = torch.where(q.abs() >= E * 2.0 ** -14, 0.0, torch.minimum(q.abs(), E * 2.0 ** -22))
@@ -40,8 +41,9 @@ def tolerance(q, k, v, tail, scale, code, out):
     digits = 2.0 ** -24 * (logit.abs() + 2.0 ** -6 * E * k.abs().sum(-1) * scale)
     d = dq @ k.abs().T * scale * stored + 2.0 ** -21 * (logit.abs() + logit.abs().amax(-1, keepdim=True))
     d = d + (torch.where(stored > 0, digits, summed) if code == K.INT8 else summed)
-    p = torch.softmax(logit, -1)
+    p = torch.softmax(logit + times.log(), -1)
     want, size = p @ v, p @ v.abs()
+    n = float(times.sum())
     term = 2.0 ** -20 + 2.0 ** -23 * min(n, 16) + 2.0 ** -24 * (n / 128)
     half = 2.0 ** -8 if out == "bf16" else 3 * 2.0 ** -24
     moved = (p * d) @ v.abs() + (p * d).sum(-1, keepdim=True) * want.abs()
