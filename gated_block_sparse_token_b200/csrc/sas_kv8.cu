@@ -358,8 +358,8 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 }
 
 // The query of one head (this lane: 32 of its values as 16 bf16 pairs) as B
-// fragments; set() takes the biased exponent e (1 .. 254) of the head's largest
-// value and returns the unit that the fragments count in.
+// fragments, in units of kUnit E: E the power of two below the head's largest
+// value, of biased exponent e (1 .. 254), which set() takes.
 __device__ __forceinline__ float pow2_down(uint32_t e) {  // 2^(127 - e), e = 254: below the normal range
   return __uint_as_float(e < 254u ? (254u - e) << 23 : 0x00400000u);
 }
@@ -367,12 +367,12 @@ __device__ __forceinline__ float pow2_down(uint32_t e) {  // 2^(127 - e), e = 25
 template <int CODE>
 struct KaQuery {  // int8: sum_n 256^n digit_n; k-step j: b[.][2j], b[.][2j + 1]
   static constexpr int kDigits = 3;
+  // largest value to below 2^22, the most that `magic` leaves room for, and a bit
+  // less than three signed bytes hold
+  static constexpr float kUnit = 1.f / 2097152.f;
   uint32_t b[kDigits][8];
 
-  __device__ __forceinline__ float set(const uint32_t (&raw)[16], uint32_t e) {
-    // largest value to below 2^22, the most that `magic` leaves room for, and a bit
-    // less than three signed bytes hold
-    constexpr float top = 2097152.f;
+  __device__ __forceinline__ void set(const uint32_t (&raw)[16], uint32_t e) {
     constexpr float magic = 12582912.f;  // 1.5 * 2^23: its sum holds the rounded value in the low bits
     constexpr uint32_t bias = 0x808080u;
     const float dn = pow2_down(e);
@@ -382,7 +382,7 @@ struct KaQuery {  // int8: sum_n 256^n digit_n; k-step j: b[.][2j], b[.][2j + 1]
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t w = raw[2 * i + (k >> 1)];
-        const float y = fmaf(((k & 1) ? bf16_hi(w) : bf16_lo(w)) * dn, top, magic);
+        const float y = fmaf(((k & 1) ? bf16_hi(w) : bf16_lo(w)) * dn, 1.f / kUnit, magic);
         u[k] = (__float_as_uint(y) - __float_as_uint(magic) + bias) ^ bias;
       }
 #pragma unroll
@@ -391,18 +391,17 @@ struct KaQuery {  // int8: sum_n 256^n digit_n; k-step j: b[.][2j], b[.][2j + 1]
         b[n][i] = __byte_perm(__byte_perm(u[0], u[1], sel), __byte_perm(u[2], u[3], sel), 0x5410);
       }
     }
-    return __uint_as_float(e << 23) * (1.f / top);
   }
 };
 template <>
 struct KaQuery<kCodeE4m3> {  // f16; k-step j: b[2j], b[2j + 1]
+  static constexpr float kUnit = 1.f;
   uint32_t b[16];
 
-  __device__ __forceinline__ float set(const uint32_t (&raw)[16], uint32_t e) {
+  __device__ __forceinline__ void set(const uint32_t (&raw)[16], uint32_t e) {
     const float dn = pow2_down(e);  // q dn lies in (-2, 2)
 #pragma unroll
     for (int i = 0; i < 16; ++i) b[i] = pack_f16x2(bf16_lo(raw[i]) * dn, bf16_hi(raw[i]) * dn);
-    return __uint_as_float(e << 23);
   }
 };
 
@@ -452,10 +451,10 @@ __device__ __forceinline__ void raise_max(KaState& st, const float (&sc)[4]) {
 // One 16-key slice of a stored block: rows at ks_addr and vs_addr in shared
 // memory, swizzled in 16-byte units by their row modulo 8.  kr: the K row of
 // this lane (key g), vr: the V rows of keys 2t and 2t + 1 (row 8 further: keys
-// g + 8, ...).
+// g + 8, ...).  qs: E of heads 2t, 2t + 1; scale: attn_scale log2(e).
 template <int CODE>
 __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint32_t vs_addr, const KaQuery<CODE>& q,
-                                             const float (&qs)[2], float ks, float vs) {
+                                             const float (&qs)[2], float scale, float ks, float vs) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int kr = (2 * (g >> 1) + (g >> 2)) ^ (4 * (g & 1)), vr = 2 * t + (t >> 1);
   uint4 x[4];
@@ -518,7 +517,9 @@ __device__ __forceinline__ void attend_codes(KaState& st, uint32_t ks_addr, uint
         codes_f16<CODE>(__byte_perm(vc[w + 2], vd[w + 2], sel), a[j][3], a[j + 1][3]);
       }
   }
-  const float f0 = qs[0] * ks, f1 = qs[1] * ks;
+  // E and the keys' scale first, like the product of query and key: neither E nor
+  // the scale alone meets a factor that could take it out of range
+  const float f0 = qs[0] * ks * (scale * KaQuery<CODE>::kUnit), f1 = qs[1] * ks * (scale * KaQuery<CODE>::kUnit);
   vs *= kKaUnshift;
 #pragma unroll
   for (int e = 0; e < 4; ++e) sc[e] *= (e & 1) ? f1 : f0;
@@ -804,10 +805,11 @@ __global__ void __launch_bounds__(32 * kKaWarps, 2)
     mag = max(mag & 0xffffu, mag >> 16);
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
     mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
-    float unit = qf.set(raw, min(max(mag >> 7, 1u), 254u));
-    if (mag >= kBf16Inf) unit = __uint_as_float(0x7fc00000u);  // an infinity or NaN: every logit is NaN
-    qs[0] = __shfl_sync(0xffffffffu, unit, 8 * t) * p.scale_log2;
-    qs[1] = __shfl_sync(0xffffffffu, unit, 8 * t + 4) * p.scale_log2;
+    const uint32_t e = min(max(mag >> 7, 1u), 254u);
+    qf.set(raw, e);
+    const float E = __uint_as_float(mag >= kBf16Inf ? 0x7fc00000u : e << 23);  // an infinity or NaN: every logit is NaN
+    qs[0] = __shfl_sync(0xffffffffu, E, 8 * t);
+    qs[1] = __shfl_sync(0xffffffffu, E, 8 * t + 4);
   }
 
   KaState st;
@@ -838,7 +840,7 @@ __global__ void __launch_bounds__(32 * kKaWarps, 2)
     }
     cp_async_wait<kKaStages - 1>();
     __syncwarp();
-    attend_codes<CODE>(st, slot, slot + 16 * kDim, qf, qs, __shfl_sync(0xffffffffu, ks_c, i & 31),
+    attend_codes<CODE>(st, slot, slot + 16 * kDim, qf, qs, p.scale_log2, __shfl_sync(0xffffffffu, ks_c, i & 31),
                        __shfl_sync(0xffffffffu, vs_c, i & 31));
     __syncwarp();
     const int nxt = i + kKaStages;  // into the slot just used

@@ -69,3 +69,15 @@ def test_dominant_query_channel(code, out, peak):
 def test_terms_of_p(code, stored):
     """Exact logits: what the terms of P leave is all there is."""
     check(N.one_channel(code, stored, DEV), code, "f32")
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("low", [0, -60, -117, 117])
+def test_queries_and_keys_at_opposite_ends(code, low):
+    """Queries 2^low, keys as much larger or smaller: their products, and so the bounds, are those of low = 0."""
+    lens = [640 + 7]
+    kv = K.make_cache(1, 1, 11, code, False, lens, "cpu", seed=9)
+    kv.k_scale.mul_(2.0 ** -low)
+    kv.k_tail.mul_(2.0 ** -low)
+    q = (torch.randn((1, 8, 128), generator=torch.Generator().manual_seed(1)).bfloat16().float() * 2.0 ** low).bfloat16()
+    check((N.moved(kv, DEV), q, 0.08), code, "f32")
