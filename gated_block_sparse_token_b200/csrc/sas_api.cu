@@ -876,15 +876,14 @@ sas_status sas_decode_step_host(const sas_config* cfg, const void* q_host, void*
 // ---------------------------------------------------------------- norms with rotation
 namespace {
 
-// Host checks of one sas_rows argument; `out` rows must not repeat.
+// Host checks of one sas_rows argument; `out` rows must not repeat.  The stride of
+// a dimension with one entry is multiplied by 0 only: it may be anything.
 sas_status check_rows(const sas_rows* r, int64_t elem, int batch, int heads, long long tokens, bool out) {
-  if (r->data == nullptr || !aligned(r->data, 16)) return SAS_ERR_INVALID_ARG;
-  if (r->seq_stride < 0 || r->token_stride < 0 || r->head_stride < 0 || r->tokens < tokens)
-    return SAS_ERR_INVALID_ARG;
-  if (r->seq_stride * elem % 16 != 0 || r->token_stride * elem % 16 != 0 || r->head_stride * elem % 16 != 0)
-    return SAS_ERR_INVALID_ARG;
-  if (out && ((batch > 1 && r->seq_stride < kDim) || (heads > 1 && r->head_stride < kDim) ||
-              (tokens > 1 && r->token_stride < kDim)))
+  if (r->data == nullptr || !aligned(r->data, 16) || r->tokens < tokens) return SAS_ERR_INVALID_ARG;
+  const auto bad = [&](bool used, int64_t stride) {
+    return used && (stride < 0 || stride * elem % 16 != 0 || (out && stride < kDim));
+  };
+  if (bad(batch > 1, r->seq_stride) || bad(heads > 1, r->head_stride) || bad(tokens > 1, r->token_stride))
     return SAS_ERR_INVALID_ARG;
   return SAS_OK;
 }
@@ -1044,8 +1043,11 @@ sas_status sas_kv8_append(const sas_config* cfg, const sas_kv8* kv, const sas_ro
   if (cfg->kv_dtype != SAS_DTYPE_BF16) return SAS_ERR_UNSUPPORTED;
   if (k_new == nullptr || v_new == nullptr || !aligned(new_starts, 4) || !aligned(new_lens, 4))
     return SAS_ERR_INVALID_ARG;
-  if ((st = check_rows(k_new, 2, kv->batch, cfg->num_kv_heads, 0, false)) != SAS_OK) return st;
-  if ((st = check_rows(v_new, 2, kv->batch, cfg->num_kv_heads, 0, false)) != SAS_OK) return st;
+  const auto check_new = [&](const sas_rows* r) {  // which of its rows are read is known on the device only
+    return check_rows(r, 2, kv->batch, cfg->num_kv_heads, std::max<long long>(r->tokens, 0), false);
+  };
+  if ((st = check_new(k_new)) != SAS_OK) return st;
+  if ((st = check_new(v_new)) != SAS_OK) return st;
   sas::Kv8AppendParams p{};
   p.kv = make_view8(cfg, kv);
   p.k_new = rows_view(k_new);

@@ -457,7 +457,8 @@ SAS_API sas_status sas_decode_step_static(const sas_config* cfg, const void* q, 
  * data + s * seq_stride + h * head_stride + t * token_stride. */
 typedef struct {
   void* data;           /* 16-byte aligned */
-  int64_t seq_stride;   /* strides >= 0, each a multiple of 16 bytes */
+  int64_t seq_stride;   /* strides >= 0, each a multiple of 16 bytes; that of a
+                           dimension with one entry is not looked at */
   int64_t token_stride;
   int64_t head_stride;
   int64_t tokens;       /* token rows that data holds per sequence */

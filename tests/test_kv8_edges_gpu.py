@@ -236,3 +236,38 @@ def test_attend_every_block_in_portions(code, out, B, blocks, chunks):
     q, o = run(kv, cfg, None, ws)
     assert status(ws) == sas.SAS_OK
     check_few_pages(kv, cfg, q, o, None, lens, code)
+
+
+def test_single_entries_with_odd_strides():
+    """One sequence, one head, one token, with whatever strides: norms, write and read-back."""
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(1, 1, 1, 128, generator=g).bfloat16().to(DEV)
+    odd = x.as_strided((1, 1, 1, 128), (3, 5, 7, 1))
+    gain = torch.ones(128, device=DEV)
+    cfg = sas.Config(1, 1)
+    a, b = torch.zeros_like(x), torch.zeros_like(x)
+    sas.qk_norm_rope(cfg, x, x, gain, gain, a, b, 1e4)
+    c, d = torch.zeros_like(x), torch.zeros_like(x)
+    sas.qk_norm_rope(cfg, odd, odd, gain, gain, c.as_strided((1, 1, 1, 128), (1, 1, 1, 1)),
+                     d.as_strided((1, 1, 1, 128), (9, 9, 9, 1)), 1e4)
+    kv = K.make_cache(1, 1, 2, K.INT8, False, [1], DEV)
+    ws = sas.make_workspace(cfg, DEV)
+    sas.kv8_append(cfg, kv, odd, odd, ws)
+    back = torch.zeros_like(x)
+    sas.kv8_read(cfg, kv, back.as_strided((1, 1, 1, 128), (1, 3, 5, 1)), None, ws)
+    assert status(ws) == sas.SAS_OK
+    assert torch.equal(a, c) and torch.equal(b, d) and torch.equal(back, x)
+
+
+@pytest.mark.parametrize("B", [1024, 1025])
+def test_attend_every_block_of_more_sequences_than_are_cut(B):
+    """The most sequences that are cut into chunks, and one more, which go by clusters."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(1, 300, (B,), generator=g).tolist()
+    lens[0], lens[1], lens[B - 1], lens[B - 2] = 64 * 70, 1, 64 * 69 + 1, 64 * 40
+    kv = few_pages(lens, 70, K.E4M3, 3)
+    cfg = sas.Config(2, 1)
+    ws = torch.zeros(sas.sparse_decode_kv8_workspace_bytes(cfg, B), dtype=torch.uint8, device=DEV)
+    q, o = run(kv, cfg, None, ws)
+    assert status(ws) == sas.SAS_OK
+    check_few_pages(kv, cfg, q, o, None, lens, K.E4M3)
