@@ -506,8 +506,7 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
 // ---------------------------------------------------------------- 8-bit codes
 enum Kv8Code : int { kCodeE4m3 = 0, kCodeInt8 = 1 };
 
-// Two e4m3 codes as f16x2;
-// exact.
+// Two e4m3 codes as f16x2 (exact).
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t x) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));

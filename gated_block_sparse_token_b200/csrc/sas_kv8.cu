@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(256, 3) kv8_append_kernel(const __grid_constan
 // threads 0-127 the keys, 128-255 the values.  A lane turns as many codes as
 // make 16 output bytes, so that a warp's stores fill whole sectors; the next
 // block's codes are requested before this one's values are stored.  Bound by
-// memory, 3 B a value into bf16: 805 MB in 129 us (6.2 TB/s).
+// memory, 3 B a value into bf16: 805 MB in 129 us (6.2 TB/s); 5 B into fp32: 1.34 GB
+// in 222 us (6.0 TB/s).
 template <int CODE, typename OutT>
 __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant__ Kv8ReadParams p) {
   constexpr int VEC = 16 / static_cast<int>(sizeof(OutT));  // codes of a lane: 8 or 4
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 // an SM whatever the register use.  (Loads into registers, one slice ahead, left
 // too little in flight: 84 us for 256 pairs x 64 blocks; a ring fed by 2-D TMA
 // from a lane of one of the consuming warps, which spends that warp's time on
-// two copies a block: 59; this one 53.)
+// two copies a block: 59; this one 55.)
 //   S^T = K q^T  the 16 keys are the rows, the (up to 8) heads of the group the
 //                columns.  int8: m16n8k32 on the codes as they are stored, the
 //                query as the three signed 8-bit digits of a fixed-point number
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 //                two products: 2^-22 of it.  (One term, 2^-11, left a few in a
 //                hundred bf16 outputs on the other side of a rounding border; it
 //                saves 2.5 of 96 us over 2 x 128k tokens, 0.5 of 11.5 on 64 pairs x
-//                32 blocks.)  It enters as 2^kKaShift p, so that this holds for every
+//                32 blocks, 11 of 185 over 16 x 32,000 tokens.)  It enters as 2^kKaShift p, so that this holds for every
 //                key down to 2^-14 of the largest, and 2^-15 down to 2^-21: a few
 //                keys that take nearly all the weight leave the others exact
 //                enough (unshifted, a hundred thousand keys at 2^-24 were a third
@@ -322,11 +323,12 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 // distributed shared memory.  Dense attention (CHUNKS): every sequence in chunks
 // of equal length, one CTA a (chunk, head), so that few or ragged long
 // sequences fill the SMs; a second kernel merges the chunks' partial sums (16
-// pairs x 2,000 blocks: 92-101 us; clusters of 8 114-121, of 16, which not every
-// GPC holds twice, 105-118).
-// Measured: 64 pairs x 32 blocks 10.9 us (3.1 TB/s; the launch, the chain of
-// length, list, table and first tile, and the merge are half of it), 256 pairs x
-// 64 blocks 54 us (5.0 TB/s), 128 pairs x 500 blocks dense 172 us (6.0 TB/s).
+// pairs x 2,000 blocks, e4m3 / int8: 95 / 94 us against 132 / 178 by clusters; 128
+// pairs x 500 blocks, which are even: 185 / 197 against 170 / 180).
+// Measured, e4m3: 64 pairs x 32 blocks 11.6 us (2.9 TB/s; the launch, the chain of
+// length, list, table and first tile, and the merge are half of it; int8 13.6), 256
+// pairs x 64 blocks 53 us (5.1 TB/s; int8 55), 128 pairs x 500 blocks dense 170 us
+// (6.2 TB/s).
 constexpr int kKaStages = 3;                // ring slots of a warp
 constexpr int kKaSlot = 2 * 16 * kDim;      // 16 rows of K, then of V
 constexpr int kKaHeadPair = 2 * kDim + 4;   // floats between head pairs of a partial (bank spread)
@@ -1067,11 +1069,12 @@ cudaError_t launch_kv8_read(int code, bool f32_out, const Kv8ReadParams& p, int 
 
 // CTAs of a cluster: as many as keep the whole grid resident at once (two of 8
 // warps an SM), up to one block a group of four warps.  Measured, CTAs a cluster
-// -> us: 64 pairs x 32 blocks 8 -> 20.8, 4 -> 11.7, 2 -> 13.8; 256 pairs x 64
-// blocks 8 -> 102, 4 -> 71, 2 -> 60, 1 -> 53.  More pairs than that run in waves:
-// two CTAs a pair shorten a last wave that is half empty or more (304 / 336 / 400
-// pairs x 64 blocks: 68 / 75 / 82 us against 72 / 83 / 86 with one; 512 and 592:
-// 103 and 118 against 98 and 115).
+// -> us: 64 pairs x 32 blocks 8 -> 17.6, 4 -> 11.7, 2 -> 14.6; 256 pairs x 64
+// blocks 8 -> 92, 4 -> 70, 2 -> 60, 1 -> 55.  More pairs than that run in waves:
+// two CTAs a pair shorten a last wave that is half empty or more (304 / 336 / 368 /
+// 400 pairs x 64 blocks, e4m3: 67 / 75 / 78 / 81 us against 73 / 85 / 86 / 88 with
+// one, int8: 74 / 76 / 79 / 87 against 81 / 83 / 83 / 84; 512 and 592 int8: 104 and
+// 120 against 104 and 115).
 int kv8_attend_cluster(int pairs, int max_blocks) {
   int cluster = 1;
   const int last = pairs % (2 * 148);

@@ -17,8 +17,9 @@
 // the angles are reduced in double precision (exact for any int32 position)
 // and would otherwise cost more than the row.  Measured, bf16, 32 + 8 heads:
 // 2 x 32,768 tokens 210 us (6.4 TB/s), one decode step of 8 sequences 2.5 us;
-// gradient of 8 x 1,021 padded tokens of 40 + 8 heads 36 us (6.2 TB/s) and 3 for
-// the gains' sum, of 2 x 32,768 tokens 302 (6.0 TB/s).
+// gradient, with the gains' sum and the caller's zeroing of them, of 8 x 1,021
+// padded tokens of 40 + 8 heads 42 us (5.4 TB/s), of 2 x 32,768 tokens 308 (6.5
+// TB/s).  fp32: 462, 85 and 630 us (5.8, 5.3 and 6.4 TB/s).
 #include "sas_internal.h"
 
 namespace sas {

@@ -635,7 +635,8 @@ def sparse_decode_kv8(cfg: Config, q, kv: KvCache8, sel_idx, sel_count, out, ws,
     """sas_sparse_decode_kv8: q bf16 [B][Hq][128], out cfg.out_dtype likewise;
     sel_idx / sel_count as topk_blocks writes them, or both None: every block
     (then with sparse_decode_kv8_workspace_bytes(cfg, B) bytes of ws, few or
-    ragged long sequences use the whole GPU)."""
+    ragged long sequences use the whole GPU, and calls that may overlap need a
+    workspace each)."""
     B, hkv = kv.batch, cfg.num_kv_heads
     _plain("q", q, (B, cfg.num_q_heads, 128), torch.bfloat16)
     _plain("out", out, (B, cfg.num_q_heads, 128), out_dtype(cfg))

@@ -475,8 +475,9 @@ typedef struct {
  *              cfg->rope_base is the gate's
  *   q, k       inputs [B][Hq][T] and [B][Hkv][T] rows; either may be NULL (and
  *              its output with it): the other alone is computed
- *   positions  int32 [B][T] on the device, or NULL: t (B * T at most 2^29).  A row whose position
- *              is negative (padding) is skipped: its output stays as it was
+ *   positions  int32 [B][T] on the device, or NULL: t (B * T at most 2^29).  A
+ *              row whose position is negative (padding) is skipped: its output
+ *              stays as it was
  *   q_out, k_out  may be the inputs themselves (same data and strides); any
  *              other overlap, and rows of one output that overlap, are the
  *              caller's error
@@ -595,7 +596,10 @@ SAS_API sas_status sas_kv8_read(const sas_config* cfg, const sas_kv8* kv, const 
  * sas_pool_keys over the 8-bit cache: the pooled keys are those of the stored
  * values (code * scale).  Same arguments and outputs; only complete blocks
  * are pooled, the current one included when it is complete (its codes are
- * written when it completes).
+ * written when it completes).  Few blocks and many take different kernels, whose
+ * fp32 sums run in different orders: unlike the codes, the gate keys of a block
+ * depend on how many are pooled in a call, in their last bits (some 1e-7 of
+ * them).  The same call gives the same bits.
  */
 SAS_API sas_status sas_pool_keys_kv8(const sas_config* cfg, const sas_kv8* kv,
                                      const int32_t* blk_begin, int32_t num_blocks,
@@ -618,8 +622,11 @@ SAS_API size_t sas_sparse_decode_kv8_workspace_bytes(const sas_config* cfg, int3
  *   out  out_dtype [B][Hq][128]
  *   ws   at least sas_workspace_bytes(cfg, 0, 0); with at least
  *        sas_sparse_decode_kv8_workspace_bytes(cfg, B), attention over every
- *        block is cut into equal chunks that a second kernel merges (calls that
- *        may overlap on the GPU then need a workspace each)
+ *        block is cut into equal chunks that a second kernel merges: the sums run
+ *        in another order, and the workspace holds them, so that calls that may
+ *        overlap on the GPU need one each (also where it is that large for
+ *        another call's sake).  With a smaller ws, and over lists, only the
+ *        status word is used
  * Logits, softmax statistics and sums are fp32.  Over the stored blocks the query
  * is exact down to 2^-14 of the power of two below its head's largest value, and
  * within 2^-22 of that below.  The probabilities enter the product with the values
