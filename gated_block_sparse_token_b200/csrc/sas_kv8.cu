@@ -303,12 +303,12 @@ __global__ void __launch_bounds__(256, 3) kv8_read_kernel(const __grid_constant_
 //                two products: 2^-22 of it.  (One term, 2^-11, left a few in a
 //                hundred bf16 outputs on the other side of a rounding border; it
 //                saves 2.5 of 96 us over 2 x 128k tokens, 0.5 of 11.5 on 64 pairs x
-//                32 blocks, 11 of 185 over 16 x 32,000 tokens.)  It enters as 2^kKaShift p, so that this holds for every
-//                key down to 2^-14 of the largest, and 2^-15 down to 2^-21: a few
-//                keys that take nearly all the weight leave the others exact
-//                enough (unshifted, a hundred thousand keys at 2^-24 were a third
-//                off).  V's scale takes the factor back.  The sum of P runs over
-//                the unrounded values.
+//                32 blocks, 11 of 185 over 16 x 32,000 tokens.)  It enters as
+//                2^kKaShift p, so that this holds for every key down to 2^-14 of the
+//                largest, and 2^-15 down to 2^-21: a few keys that take nearly all
+//                the weight leave the others exact enough (unshifted, a hundred
+//                thousand keys at 2^-24 were a third off).  V's scale takes the
+//                factor back.  The sum of P runs over the unrounded values.
 // Both products take their k index from whatever order makes a lane's 16-byte
 // shared load its fragment: dims 16t .. 16t+15 and 64 + those for K, dims 16g ..
 // of four keys for V.  Key g of a fragment is row 2(g/2) + g/4 (xor 4 for odd
